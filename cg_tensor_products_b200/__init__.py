@@ -9,6 +9,11 @@ tensors must live on a CUDA device, and a missing library raises.
     out = forward(plan, row_ptr, src, r, x, w)
     rev_ptr, rev_perm, dst = build_reverse_csr(N, row_ptr, src)
     gx, gw, gr = backward(plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, grad_out)
+
+The dense row operators (include/etp_dense.h) need no plan; they read blocks of node features in place:
+
+    h, mean, rstd = layer_norm_forward(x[:, :1], weight, bias)
+    out, z = linear_forward(h, W, b, activation="silu", residual=x[:, :1], save_z=True)
 """
 from __future__ import annotations
 
@@ -19,12 +24,15 @@ import re
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libetp.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "etp.h")
+DENSE_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "etp_dense.h")
 
 ETP_OK, ETP_ERR_INVALID_ARG, ETP_ERR_UNSUPPORTED, ETP_ERR_BAD_CSR = 0, 1, 2, 3
 ETP_ERR_CUDA, ETP_ERR_ALLOC, ETP_ERR_WORKSPACE, ETP_ERR_TOO_LARGE = 4, 5, 6, 7
 STATIC_MAX_NODES = STATIC_MAX_EDGES = 1 << 18
 FRAME_FLOATS = 88  # floats of one edge frame record (ETP_FRAME_FLOATS)
-ETP_F32 = 0
+ETP_F32, ETP_BF16 = 0, 1
+ACT_NONE, ACT_SILU = 0, 1
+LINEAR_MAX_CHANNELS, NORM_MAX_CHANNELS = 65536, 8192
 CSR_BAD_ENDPOINTS, CSR_NOT_MONOTONE, CSR_SRC_RANGE = 1, 2, 4
 
 _lib = None
@@ -75,6 +83,12 @@ def _load():
         "etp_build_locality_schedule": [i32, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "etp_forward_ordered": [vp, i32, i32] + [vp] * 10 + [sz, vp],
         "etp_backward_ordered": [vp, i32, i32] + [vp] * 13 + [sz, vp],
+        "etp_linear_forward": [i32] * 5 + [vp, vp, vp, i32, vp, vp, vp, vp],
+        "etp_linear_workspace_size": [i32] * 5 + [ctypes.POINTER(sz)],
+        "etp_linear_backward": [i32] * 5 + [vp, vp, i32] + [vp] * 6 + [sz, vp],
+        "etp_layer_norm_forward": [i32] * 4 + [ctypes.c_float] + [vp] * 7,
+        "etp_layer_norm_workspace_size": [i32] * 4 + [ctypes.POINTER(sz)],
+        "etp_layer_norm_backward": [i32] * 4 + [vp] * 9 + [sz, vp],
         "etp_device_fault": [vp],
         "etp_status_string": [i32],
     }
@@ -86,9 +100,9 @@ def _load():
     return lib
 
 
-def declared_symbols() -> list:
-    """Function names declared in include/etp.h."""
-    with open(HEADER_PATH) as f:
+def declared_symbols(header: str = HEADER_PATH) -> list:
+    """Function names declared in include/etp.h (or in another of the library's headers)."""
+    with open(header) as f:
         txt = f.read()
     return re.findall(r"ETP_API\s+[\w\s\*]+?\b(etp_\w+)\s*\(", txt)
 
@@ -417,6 +431,283 @@ def double_backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, g
             _ptr(gg_w), _ptr(gg_r), _ptr(out.get("grad_g")), _ptr(out.get("grad_x")), _ptr(out.get("grad_w")),
             _ptr(out.get("grad_r")), _ptr(workspace), workspace.numel(), stream=stream)
     return out
+
+
+class _Rows(ctypes.Structure):
+    """etp_rows: rows of channels at data + group * group_stride + row * row_stride."""
+    _fields_ = [("data", ctypes.c_void_p), ("group_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+_DENSE_TYPES = {"torch.float32": ETP_F32, "torch.bfloat16": ETP_BF16}
+_ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "silu": ACT_SILU}
+
+
+def _dense_rows(t, name: str, like=None, channels=None):
+    """etp_rows of a tensor [M, C] or [groups, rows, C] whose channels are contiguous (None for None).
+    like: the tensor whose leading sizes and dtype it must share; channels: its C."""
+    if t is None:
+        return None
+    shape = t.shape
+    nd = len(shape)
+    if nd != 2 and nd != 3:
+        raise ValueError(f"{name}: expected [rows, channels] or [groups, rows, channels], got {tuple(shape)}")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name}: expected {like.dtype}, got {t.dtype}")
+        if shape[:-1] != like.shape[:-1]:
+            raise ValueError(f"{name}: expected leading sizes {tuple(like.shape[:-1])}, got {tuple(shape[:-1])}")
+    if channels is not None and shape[-1] != channels:
+        raise ValueError(f"{name}: expected {channels} channels, got {shape[-1]}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: channels must be contiguous (stride {st[-1]})")
+    return _Rows(t.data_ptr(), st[0], st[1] if nd == 3 else 0)
+
+
+def _dense_type(x):
+    code = _DENSE_TYPES.get(str(x.dtype))
+    if code is None:
+        raise ValueError(f"x: expected float32 or bfloat16, got {x.dtype}")
+    return code
+
+
+def _dense_vector(t, name: str, like, *shape):
+    if t is None:
+        return None
+    if t.dtype != like.dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {like.dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _dense_device(*ts):
+    """The one CUDA device of the given tensors (None entries are skipped); strided rows are accepted."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors: this library has no CPU path")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices ({dev}, {t.device})")
+    return dev
+
+
+def _span(t):
+    """Elements from the first to one past the last of t."""
+    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+
+
+def _overlap(a, b) -> bool:
+    """Whether the tensors may share memory. Two blocks of one feature tensor (equal group strides)
+    whose channel ranges are apart do not."""
+    if a is None or b is None or not a.numel() or not b.numel():
+        return False
+    pa, pb, es = a.data_ptr(), b.data_ptr(), a.element_size()
+    if pa + _span(a) * es <= pb or pb + _span(b) * b.element_size() <= pa:
+        return False
+    gs = a.stride(0)
+    if a.dim() >= 2 and b.dim() >= 2 and es == b.element_size() and gs == b.stride(0) and (pb - pa) % es == 0:
+        sa, sb = (_span(t) - (t.shape[0] - 1) * gs for t in (a, b))
+        d = ((pb - pa) // es) % gs if gs else 0
+        if gs and d >= sa and d + sb <= gs:
+            return False
+    return True
+
+
+def _same_rows(a, b) -> bool:
+    return b is not None and a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+
+
+def _dense_outputs(outs, ins, in_place=()):
+    """Raise ValueError when a caller's output overlaps an input or another output. in_place: (output, input)
+    names that may be the very same tensor."""
+    outs = [(n, t) for n, t in outs if t is not None]
+    for i, (n, t) in enumerate(outs):
+        for m, u in list(ins) + outs[:i]:
+            if _overlap(t, u) and not ((n, m) in in_place and _same_rows(t, u)):
+                raise ValueError(f"{n} must not overlap {m}")
+
+
+def _check_workspace(workspace):
+    _expect(workspace, "workspace", "uint8", (None,))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+
+
+def _dense_shape(x):
+    """(groups, per_group) of x's rows."""
+    return (x.shape[0], 1) if x.dim() == 2 else (x.shape[0], x.shape[1])
+
+
+def _check_linear(x, W, activation):
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation: expected 'none' or 'silu', got {activation!r}")
+    if W.dim() != 2 or not 1 <= W.shape[0] <= LINEAR_MAX_CHANNELS or not 1 <= W.shape[1] <= LINEAR_MAX_CHANNELS:
+        raise ValueError(f"W: expected [K, N] with 1 <= K, N <= {LINEAR_MAX_CHANNELS}, got {tuple(W.shape)}")
+    return _ACTIVATIONS[activation]
+
+
+def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=False, z=None, out=None, stream=None):
+    """out = act(x W + bias) + residual (launches etp_linear_forward). x [M, K] or [groups, rows, K], rows at any
+    stride (a block x[:, l*l:(l+1)**2] of node features is read in place); W [K, N]; float32 or bfloat16, one type
+    for all. activation: 'none' or 'silu'. save_z=True (or z given) also keeps z = x W + bias for linear_backward:
+    returns (out, z). out may be residual itself."""
+    import torch
+
+    code = _dense_type(x)
+    act = _check_linear(x, W, activation)
+    K, N = W.shape
+    xr = _dense_rows(x, "x", None, K)
+    Wp = _dense_vector(W, "W", x, K, N)
+    bp = _dense_vector(bias, "bias", x, N)
+    rr = _dense_rows(residual, "residual", x, N)
+    if out is not None or z is not None:
+        _dense_outputs([("out", out), ("z", z)], [("x", x), ("W", W), ("bias", bias), ("residual", residual)],
+                       {("out", "residual")})
+    if out is None:
+        out = torch.empty((*x.shape[:-1], N), device=x.device, dtype=x.dtype)
+    if z is None and save_z:
+        z = torch.empty((*x.shape[:-1], N), device=x.device, dtype=x.dtype)
+    orow, zr = _dense_rows(out, "out", x, N), _dense_rows(z, "z", x, N)
+    dev = _dense_device(x, W, bias, residual, z, out)
+    _launch(dev, "etp_linear_forward", _load().etp_linear_forward, code, *_dense_shape(x), K, N, ctypes.byref(xr), Wp,
+            bp, act, rr and ctypes.byref(rr), zr and ctypes.byref(zr), ctypes.byref(orow), stream=stream)
+    return out if z is None else (out, z)
+
+
+def linear_workspace_size(M: int, K: int, N: int, dtype="float32", device=None) -> int:
+    """Bytes of workspace linear_backward needs for M rows (etp_linear_workspace_size on `device`)."""
+    import torch
+
+    b = ctypes.c_size_t()
+    code = _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")]
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(_load().etp_linear_workspace_size(code, int(M), 1, int(K), int(N), ctypes.byref(b)),
+               "etp_linear_workspace_size")
+    return b.value
+
+
+def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "bias"), grad_x=None, grad_W=None,
+                    grad_bias=None, workspace=None, stream=None):
+    """(grad_x, grad_W, grad_bias) of linear_forward for the cotangent grad_out (launches etp_linear_backward);
+    unwanted ones are None. z: what linear_forward kept (needed for 'silu'). The residual's gradient is grad_out."""
+    import torch
+
+    code = _dense_type(x)
+    act = _check_linear(x, W, activation)
+    K, N = W.shape
+    if act == ACT_NONE:
+        z = None
+    elif z is None:
+        raise ValueError("z: the forward's pre-activation is needed for this activation")
+    xr, Wp = _dense_rows(x, "x", None, K), _dense_vector(W, "W", x, K, N)
+    gr, zr = _dense_rows(grad_out, "grad_out", x, N), _dense_rows(z, "z", x, N)
+    if grad_x is not None or grad_W is not None or grad_bias is not None:
+        _dense_outputs([("grad_x", grad_x), ("grad_W", grad_W), ("grad_bias", grad_bias)],
+                       [("x", x), ("W", W), ("grad_out", grad_out), ("z", z)])
+    if "x" in want and grad_x is None:
+        grad_x = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    if "W" in want and grad_W is None:
+        grad_W = torch.empty((K, N), device=x.device, dtype=x.dtype)
+    if "bias" in want and grad_bias is None:
+        grad_bias = torch.empty(N, device=x.device, dtype=x.dtype)
+    gxr = _dense_rows(grad_x, "grad_x", x, K)
+    gWp, gbp = _dense_vector(grad_W, "grad_W", x, K, N), _dense_vector(grad_bias, "grad_bias", x, N)
+    dev = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
+    groups, per = _dense_shape(x)
+    if workspace is None and (grad_W is not None or grad_bias is not None):
+        workspace = torch.empty(max(linear_workspace_size(groups * per, K, N, x.dtype, dev), 16), dtype=torch.uint8,
+                                device=dev)
+    _check_workspace(workspace)
+    _launch(dev, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, ctypes.byref(xr), Wp, act,
+            zr and ctypes.byref(zr), ctypes.byref(gr), gxr and ctypes.byref(gxr), gWp, gbp, _ptr(workspace),
+            0 if workspace is None else workspace.numel(), stream=stream)
+    return grad_x, grad_W, grad_bias
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
+    """(out, mean, rstd): each row of x normalised over its channels, times weight, plus bias (launches
+    etp_layer_norm_forward). x [M, C] or [groups, rows, C], rows at any stride; mean, rstd float32 [M] or
+    [groups, rows]. out may be x itself."""
+    import torch
+
+    code = _dense_type(x)
+    C = x.shape[-1] if x.dim() else 0
+    xr = _dense_rows(x, "x")
+    wp, bp = _dense_vector(weight, "weight", x, C), _dense_vector(bias, "bias", x, C)
+    if out is not None or mean is not None or rstd is not None:
+        _dense_outputs([("out", out), ("mean", mean), ("rstd", rstd)], [("x", x), ("weight", weight), ("bias", bias)],
+                       {("out", "x")})
+    if out is None:
+        out = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    if mean is None:
+        mean = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+    orow = _dense_rows(out, "out", x, C)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _expect(t, name, "float32", tuple(x.shape[:-1]))
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    dev = _dense_device(x, weight, bias, out, mean, rstd)
+    _launch(dev, "etp_layer_norm_forward", _load().etp_layer_norm_forward, code, *_dense_shape(x), C, float(eps),
+            ctypes.byref(xr), wp, bp, ctypes.byref(orow), _ptr(mean), _ptr(rstd), stream=stream)
+    return out, mean, rstd
+
+
+def layer_norm_workspace_size(M: int, C: int, dtype="float32", device=None) -> int:
+    """Bytes of workspace layer_norm_backward needs for M rows (etp_layer_norm_workspace_size on `device`)."""
+    import torch
+
+    b = ctypes.c_size_t()
+    code = _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")]
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(_load().etp_layer_norm_workspace_size(code, int(M), 1, int(C), ctypes.byref(b)),
+               "etp_layer_norm_workspace_size")
+    return b.value
+
+
+def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "bias"), grad_x=None, grad_weight=None,
+                        grad_bias=None, workspace=None, stream=None):
+    """(grad_x, grad_weight, grad_bias) of layer_norm_forward for the cotangent grad_out (launches
+    etp_layer_norm_backward); unwanted ones are None. weight: as in the forward (None: ones); mean, rstd: what it
+    returned. grad_x may be grad_out or x itself."""
+    import torch
+
+    code = _dense_type(x)
+    C = x.shape[-1] if x.dim() else 0
+    xr, gr = _dense_rows(x, "x"), _dense_rows(grad_out, "grad_out", x, C)
+    wp = _dense_vector(weight, "weight", x, C)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _expect(t, name, "float32", tuple(x.shape[:-1]))
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    if grad_x is not None or grad_weight is not None or grad_bias is not None:
+        _dense_outputs([("grad_x", grad_x), ("grad_weight", grad_weight), ("grad_bias", grad_bias)],
+                       [("x", x), ("weight", weight), ("mean", mean), ("rstd", rstd), ("grad_out", grad_out)],
+                       {("grad_x", "x"), ("grad_x", "grad_out")})
+    if "x" in want and grad_x is None:
+        grad_x = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    if "weight" in want and grad_weight is None:
+        grad_weight = torch.empty(C, device=x.device, dtype=x.dtype)
+    if "bias" in want and grad_bias is None:
+        grad_bias = torch.empty(C, device=x.device, dtype=x.dtype)
+    gxr = _dense_rows(grad_x, "grad_x", x, C)
+    gwp, gbp = _dense_vector(grad_weight, "grad_weight", x, C), _dense_vector(grad_bias, "grad_bias", x, C)
+    dev = _dense_device(x, weight, mean, rstd, grad_out, grad_x, grad_weight, grad_bias, workspace)
+    groups, per = _dense_shape(x)
+    if workspace is None and (grad_weight is not None or grad_bias is not None):
+        workspace = torch.empty(max(layer_norm_workspace_size(groups * per, C, x.dtype, dev), 16), dtype=torch.uint8,
+                                device=dev)
+    _check_workspace(workspace)
+    _launch(dev, "etp_layer_norm_backward", _load().etp_layer_norm_backward, code, groups, per, C, ctypes.byref(xr), wp,
+            _ptr(mean), _ptr(rstd), ctypes.byref(gr), gxr and ctypes.byref(gxr), gwp, gbp, _ptr(workspace),
+            0 if workspace is None else workspace.numel(), stream=stream)
+    return grad_x, grad_weight, grad_bias
 
 
 def assemble_forces(N: int, row_ptr, rev_ptr, rev_perm, grad_r, r=None, forces=None, virial=None, stream=None):

@@ -23,7 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 GEN_DIR = os.path.join(CSRC, "generated")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libetp.so")
-HEADER = os.path.join(ROOT, "include", "etp.h")
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("etp.h", "etp_dense.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "--expt-relaxed-constexpr", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -39,7 +39,7 @@ def _nvcc() -> str:
 
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp")) + [HEADER])
+                  glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp")) + HEADERS)
 
 
 def up_to_date() -> bool:
@@ -80,8 +80,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     for L in range(4):
         jobs.append((os.path.join(CSRC, "etp_kernels_inst.cu"), os.path.join(BUILD_DIR, f"etp_kernels_l{L}.o"),
                      [f"-DETP_L={L}"]))
-    for name in ("etp_graph", "etp_forces", "etp_radial", "etp_radial_tc", "etp_fused", "etp_double", "etp_cart", "etp_nodeprod", "etp_api",
-                 "etp_static_scratch", "etp_launch"):
+    for name in ("etp_graph", "etp_forces", "etp_radial", "etp_radial_tc", "etp_fused", "etp_double", "etp_cart", "etp_nodeprod",
+                 "etp_norm", "etp_linear", "etp_dense_api", "etp_api", "etp_static_scratch", "etp_launch"):
         jobs.append((os.path.join(CSRC, name + ".cu"), os.path.join(BUILD_DIR, name + ".o"), []))
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 

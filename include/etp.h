@@ -81,7 +81,10 @@ extern "C" {
 typedef struct etp_plan_s* etp_plan_t;
 typedef struct CUstream_st* etp_stream_t; /* a cudaStream_t; NULL is the legacy default stream */
 
-typedef enum { ETP_F32 = 0 } etp_dtype;
+typedef enum {
+    ETP_F32 = 0,
+    ETP_BF16 = 1 /* bfloat16: the dense row operators of etp_dense.h only */
+} etp_dtype;
 
 typedef enum {
     ETP_OK = 0,
