@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "etp.h"
+#include "etp_dense.cuh"
 #include "etp_device.cuh"
 #include "etp_internal.h"
 
@@ -631,8 +632,9 @@ etp_status etp_device_fault(int* fault) {
     const int f0 = etp::read_and_clear_fault<0>(), f1 = etp::read_and_clear_fault<1>();
     const int f2 = etp::read_and_clear_fault<2>(), f3 = etp::read_and_clear_fault<3>();
     const int f4 = etp::radial_tc_read_and_clear_fault(), f5 = etp::fused_read_and_clear_fault();
-    if (f0 < 0 || f1 < 0 || f2 < 0 || f3 < 0 || f4 < 0 || f5 < 0) return ETP_ERR_CUDA;
-    *fault = f0 | f1 | f2 | f3 | f4 | f5;
+    const int f6 = etp::dense::linear_read_and_clear_fault();
+    if (f0 < 0 || f1 < 0 || f2 < 0 || f3 < 0 || f4 < 0 || f5 < 0 || f6 < 0) return ETP_ERR_CUDA;
+    *fault = f0 | f1 | f2 | f3 | f4 | f5 | f6;
     return ETP_OK;
 }
 

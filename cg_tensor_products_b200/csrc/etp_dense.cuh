@@ -92,7 +92,7 @@ struct Pack<__nv_bfloat16, 8> {
 
 // SiLU and its derivative in float32: s = 1 / (1 + exp(-z)), silu = z s,
 // silu' = s (1 + z (1 - s)). 1 / inf is 0, so large negative z give 0.
-__device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 __device__ __forceinline__ float silu_grad(float z) {
     const float s = sigmoid(z);
@@ -121,8 +121,9 @@ struct LinearArgs {
     bool silu;
 };
 cudaError_t linear_forward(bool bf16, const LinearArgs& a, cudaStream_t s);
-size_t linear_workspace_bytes(bool bf16, int M, int K, int N);
+size_t linear_workspace_bytes(int M, int K, int N);
 cudaError_t linear_backward(bool bf16, const LinearArgs& a, cudaStream_t s);
+int linear_read_and_clear_fault();
 
 }  // namespace dense
 }  // namespace etp

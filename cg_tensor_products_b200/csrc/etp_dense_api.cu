@@ -115,7 +115,7 @@ etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group,
     if (c.status != ETP_OK) return c.status;
     if (!bytes || K < 1 || N < 1 || K > ETP_LINEAR_MAX_CHANNELS || N > ETP_LINEAR_MAX_CHANNELS)
         return ETP_ERR_INVALID_ARG;
-    *bytes = etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N);
+    *bytes = etp::dense::linear_workspace_bytes(c.map.M, K, N);
     return ETP_OK;
 }
 
@@ -139,7 +139,7 @@ etp_status etp_linear_backward(etp_dtype dtype, int groups, int per_group, int K
         if (grad_W && !c.rows(x, K, false, &a.x)) return ETP_ERR_INVALID_ARG;
     }
     if (grad_W || grad_bias) {
-        const size_t need = etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N);
+        const size_t need = etp::dense::linear_workspace_bytes(c.map.M, K, N);
         if (need > 0 && (!workspace || !aligned(workspace, 16))) return ETP_ERR_INVALID_ARG;
         if (workspace_bytes < need) return ETP_ERR_WORKSPACE;
     }
