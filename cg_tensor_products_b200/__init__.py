@@ -83,7 +83,7 @@ def _load():
         "etp_build_locality_schedule": [i32, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "etp_forward_ordered": [vp, i32, i32] + [vp] * 10 + [sz, vp],
         "etp_backward_ordered": [vp, i32, i32] + [vp] * 13 + [sz, vp],
-        "etp_linear_forward": [i32] * 5 + [vp, vp, vp, i32, vp, vp, vp, vp],
+        "etp_linear_forward": [i32] * 5 + [vp, vp, vp, i32, vp, vp, vp, vp, sz, vp],
         "etp_linear_workspace_size": [i32] * 5 + [ctypes.POINTER(sz)],
         "etp_linear_backward": [i32] * 5 + [vp, vp, i32] + [vp] * 6 + [sz, vp],
         "etp_layer_norm_forward": [i32] * 4 + [ctypes.c_float] + [vp] * 7,
@@ -551,11 +551,40 @@ def _check_linear(x, W, activation):
     return _ACTIVATIONS[activation]
 
 
-def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=False, z=None, out=None, stream=None):
+def linear_workspace_size(M: int, K: int, N: int, dtype="float32", device=None) -> int:
+    """Bytes of workspace linear_forward and linear_backward need for M rows (etp_linear_workspace_size on `device`)."""
+    import torch
+
+    b = ctypes.c_size_t()
+    code = _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")]
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(_load().etp_linear_workspace_size(code, int(M), 1, int(K), int(N), ctypes.byref(b)),
+               "etp_linear_workspace_size")
+    return b.value
+
+
+def _linear_workspace(code, groups, per, K, N, workspace, dev):
+    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any."""
+    import torch
+
+    if workspace is not None:
+        _check_workspace(workspace)
+        return workspace, workspace.numel()
+    b = ctypes.c_size_t()
+    with torch.cuda.device(dev):
+        _check(_load().etp_linear_workspace_size(code, groups, per, K, N, ctypes.byref(b)), "etp_linear_workspace_size")
+    if b.value == 0:
+        return None, 0
+    return torch.empty(b.value, dtype=torch.uint8, device=dev), b.value
+
+
+def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=False, z=None, out=None,
+                   workspace=None, stream=None):
     """out = act(x W + bias) + residual (launches etp_linear_forward). x [M, K] or [groups, rows, K], rows at any
     stride (a block x[:, l*l:(l+1)**2] of node features is read in place); W [K, N]; float32 or bfloat16, one type
     for all. activation: 'none' or 'silu'. save_z=True (or z given) also keeps z = x W + bias for linear_backward:
-    returns (out, z). out may be residual itself."""
+    returns (out, z). out may be residual itself. workspace: uint8 device tensor of linear_workspace_size bytes
+    (allocated when None)."""
     import torch
 
     code = _dense_type(x)
@@ -573,22 +602,13 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     if z is None and save_z:
         z = torch.empty((*x.shape[:-1], N), device=x.device, dtype=x.dtype)
     orow, zr = _dense_rows(out, "out", x, N), _dense_rows(z, "z", x, N)
-    dev = _dense_device(x, W, bias, residual, z, out)
-    _launch(dev, "etp_linear_forward", _load().etp_linear_forward, code, *_dense_shape(x), K, N, ctypes.byref(xr), Wp,
-            bp, act, rr and ctypes.byref(rr), zr and ctypes.byref(zr), ctypes.byref(orow), stream=stream)
+    dev = _dense_device(x, W, bias, residual, z, out, workspace)
+    groups, per = _dense_shape(x)
+    workspace, nbytes = _linear_workspace(code, groups, per, K, N, workspace, dev)
+    _launch(dev, "etp_linear_forward", _load().etp_linear_forward, code, groups, per, K, N, ctypes.byref(xr), Wp,
+            bp, act, rr and ctypes.byref(rr), zr and ctypes.byref(zr), ctypes.byref(orow), _ptr(workspace), nbytes,
+            stream=stream)
     return out if z is None else (out, z)
-
-
-def linear_workspace_size(M: int, K: int, N: int, dtype="float32", device=None) -> int:
-    """Bytes of workspace linear_backward needs for M rows (etp_linear_workspace_size on `device`)."""
-    import torch
-
-    b = ctypes.c_size_t()
-    code = _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")]
-    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        _check(_load().etp_linear_workspace_size(code, int(M), 1, int(K), int(N), ctypes.byref(b)),
-               "etp_linear_workspace_size")
-    return b.value
 
 
 def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "bias"), grad_x=None, grad_W=None,
@@ -619,13 +639,10 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
     gWp, gbp = _dense_vector(grad_W, "grad_W", x, K, N), _dense_vector(grad_bias, "grad_bias", x, N)
     dev = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
     groups, per = _dense_shape(x)
-    if workspace is None and (grad_W is not None or grad_bias is not None):
-        workspace = torch.empty(max(linear_workspace_size(groups * per, K, N, x.dtype, dev), 16), dtype=torch.uint8,
-                                device=dev)
-    _check_workspace(workspace)
+    workspace, nbytes = _linear_workspace(code, groups, per, K, N, workspace, dev)
     _launch(dev, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, ctypes.byref(xr), Wp, act,
             zr and ctypes.byref(zr), ctypes.byref(gr), gxr and ctypes.byref(gxr), gWp, gbp, _ptr(workspace),
-            0 if workspace is None else workspace.numel(), stream=stream)
+            nbytes, stream=stream)
     return grad_x, grad_W, grad_bias
 
 

@@ -26,20 +26,23 @@ struct FastDiv {
         mul = (unsigned)(((1ull << p) + div - 1) / div);
         shift = p - 32;
     }
-    __device__ __forceinline__ int quot(int n) const { return d == 1 ? n : (int)(__umulhi((unsigned)n, mul) >> shift); }
+    __device__ __forceinline__ unsigned quot(unsigned n) const {
+        return d == 1 ? n : (__umulhi(n, mul) >> shift);
+    }
 };
 
-// M rows in groups: row r of an operand starts at p + offset(map, r) elements.
+// M rows in groups: row r of an operand starts at p + offset(map, r) elements. Strides
+// are below 2^31 elements, so that an offset is two 32 x 32 -> 64 bit products.
 struct RowMap {
     int M = 0;
     FastDiv per;
 };
 struct Rows {
     void* p = nullptr;
-    long long gs = 0, rs = 0;
-    __device__ __forceinline__ long long offset(const RowMap& m, int r) const {
-        const int g = m.per.quot(r);
-        return (long long)g * gs + (long long)(r - g * m.per.d) * rs;
+    unsigned gs = 0, rs = 0;
+    __device__ __forceinline__ unsigned long long offset(const RowMap& m, int r) const {
+        const unsigned g = m.per.quot((unsigned)r);
+        return (unsigned long long)g * gs + (unsigned long long)((unsigned)r - g * (unsigned)m.per.d) * rs;
     }
 };
 
@@ -91,8 +94,15 @@ struct Pack<__nv_bfloat16, 8> {
 };
 
 // SiLU and its derivative in float32: s = 1 / (1 + exp(-z)), silu = z s,
-// silu' = s (1 + z (1 - s)). 1 / inf is 0, so large negative z give 0.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// silu' = s (1 + z (1 - s)), with the approximate 2^x and 1/x of the special function
+// unit (2 ulp and 1 ulp of their own results). Subnormal intermediates go to zero, which
+// only exp(-z) for z > 87 and 1/x for z < -87 reach: s is then 1 or 0 within 2^-126.
+__device__ __forceinline__ float sigmoid(float z) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
+}
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 __device__ __forceinline__ float silu_grad(float z) {
     const float s = sigmoid(z);
@@ -121,7 +131,8 @@ struct LinearArgs {
     bool silu;
 };
 cudaError_t linear_forward(bool bf16, const LinearArgs& a, cudaStream_t s);
-size_t linear_workspace_bytes(int M, int K, int N);
+// Workspace of a forward, or of a backward with these outputs.
+size_t linear_workspace_bytes(bool bf16, int M, int K, int N, bool fwd, bool gx, bool gw, bool gb);
 cudaError_t linear_backward(bool bf16, const LinearArgs& a, cudaStream_t s);
 int linear_read_and_clear_fault();
 

@@ -32,6 +32,12 @@ using etp::dense::Rows;
 etp_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ETP_OK : ETP_ERR_CUDA; }
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+etp_status check_workspace(const void* p, size_t have, size_t need) {
+    if (need == 0) return ETP_OK;
+    if (!p || !aligned(p, 16)) return ETP_ERR_INVALID_ARG;
+    return have < need ? ETP_ERR_WORKSPACE : ETP_OK;
+}
+
 // The rows of a call in the fewest groups: one group of many rows counts as many groups of one row.
 struct Call {
     RowMap map;
@@ -63,8 +69,7 @@ struct Call {
         if (!r || !r->data || !aligned(r->data, elem)) return false;
         const int64_t gs = groups_ > 1 ? r->group_stride : 0, rs = per_ > 1 ? r->row_stride : 0;
         if (gs < 0 || rs < 0) return false;
-        const int64_t most = (int64_t)1 << 40;  // offsets stay far below 2^63
-        if (gs > most || rs > most) return false;
+        if (gs > INT32_MAX || rs > INT32_MAX) return false;
         if (output) {
             const int64_t G = groups_, P = per_;
             const bool in_group = P == 1 || rs >= channels, across = G == 1 || gs >= channels;
@@ -72,13 +77,13 @@ struct Call {
             if (G > 1 && P > 1 && gs < (P - 1) * rs + channels && rs < (G - 1) * gs + channels) return false;
         }
         o->p = r->data;
-        o->gs = merged ? rs : gs;
-        o->rs = merged ? 0 : rs;
+        o->gs = (unsigned)(merged ? rs : gs);
+        o->rs = (unsigned)(merged ? 0 : rs);
         return true;
     }
     // Whether every row of the operand starts on a 16-byte boundary.
     bool v16(const Rows& r) const {
-        const long long n = 16 / (long long)elem;
+        const unsigned n = 16 / (unsigned)elem;
         return !r.p || (aligned(r.p, 16) && r.gs % n == 0 && r.rs % n == 0);
     }
 
@@ -92,7 +97,8 @@ extern "C" {
 
 etp_status etp_linear_forward(etp_dtype dtype, int groups, int per_group, int K, int N, const etp_rows* x,
                               const void* W, const void* bias, etp_activation act, const etp_rows* residual,
-                              const etp_rows* z, const etp_rows* out, etp_stream_t stream) {
+                              const etp_rows* z, const etp_rows* out, void* workspace, size_t workspace_bytes,
+                              etp_stream_t stream) {
     const Call c(dtype, groups, per_group);
     if (c.status != ETP_OK) return c.status;
     if (K < 1 || N < 1 || K > ETP_LINEAR_MAX_CHANNELS || N > ETP_LINEAR_MAX_CHANNELS) return ETP_ERR_INVALID_ARG;
@@ -106,6 +112,11 @@ etp_status etp_linear_forward(etp_dtype dtype, int groups, int per_group, int K,
     if (z && !c.rows(z, N, true, &a.z)) return ETP_ERR_INVALID_ARG;
     if (!W || !aligned(W, c.elem) || !aligned(bias, c.elem)) return ETP_ERR_INVALID_ARG;
     a.W = W, a.bias = bias;
+    const etp_status ws =
+        check_workspace(workspace, workspace_bytes,
+                        etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N, true, false, false, false));
+    if (ws != ETP_OK) return ws;
+    a.ws = static_cast<float*>(workspace);
     a.silu = act == ETP_ACT_SILU;
     return cuda_status(etp::dense::linear_forward(dtype == ETP_BF16, a, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -115,7 +126,10 @@ etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group,
     if (c.status != ETP_OK) return c.status;
     if (!bytes || K < 1 || N < 1 || K > ETP_LINEAR_MAX_CHANNELS || N > ETP_LINEAR_MAX_CHANNELS)
         return ETP_ERR_INVALID_ARG;
-    *bytes = etp::dense::linear_workspace_bytes(c.map.M, K, N);
+    // the backward of the bias alone takes ranges of its own
+    const size_t all = etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N, true, true, true, true);
+    const size_t bias = etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N, false, false, false, true);
+    *bytes = all > bias ? all : bias;
     return ETP_OK;
 }
 
@@ -138,11 +152,11 @@ etp_status etp_linear_backward(etp_dtype dtype, int groups, int per_group, int K
         if (grad_x && (!c.rows(grad_x, K, true, &a.gx) || !W || !aligned(W, c.elem))) return ETP_ERR_INVALID_ARG;
         if (grad_W && !c.rows(x, K, false, &a.x)) return ETP_ERR_INVALID_ARG;
     }
-    if (grad_W || grad_bias) {
-        const size_t need = etp::dense::linear_workspace_bytes(c.map.M, K, N);
-        if (need > 0 && (!workspace || !aligned(workspace, 16))) return ETP_ERR_INVALID_ARG;
-        if (workspace_bytes < need) return ETP_ERR_WORKSPACE;
-    }
+    const etp_status ws = check_workspace(
+        workspace, workspace_bytes,
+        etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N, false, grad_x != nullptr,
+                                           grad_W != nullptr, grad_bias != nullptr));
+    if (ws != ETP_OK) return ws;
     a.W = W;
     a.gW = grad_W, a.gbias = grad_bias;
     a.ws = static_cast<float*>(workspace);
@@ -194,9 +208,8 @@ etp_status etp_layer_norm_backward(etp_dtype dtype, int groups, int per_group, i
         if (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)) return ETP_ERR_INVALID_ARG;
     }
     if (grad_weight || grad_bias) {
-        const size_t need = etp::dense::norm_workspace_bytes(c.map.M, C);
-        if (need > 0 && (!workspace || !aligned(workspace, 16))) return ETP_ERR_INVALID_ARG;
-        if (workspace_bytes < need) return ETP_ERR_WORKSPACE;
+        const etp_status ws = check_workspace(workspace, workspace_bytes, etp::dense::norm_workspace_bytes(c.map.M, C));
+        if (ws != ETP_OK) return ws;
     }
     const bool v16 = c.v16(xr) && c.v16(gr) && c.v16(gx) && aligned(weight, 16) && (C * c.elem) % 16 == 0;
     return cuda_status(etp::dense::norm_backward(dtype == ETP_BF16, v16, c.map, C, xr, weight, mean, rstd, gr, gx,

@@ -11,9 +11,7 @@
 //     the tensor core: an operand whose contraction index is contiguous in memory
 //     K-major, one whose other index is contiguous MN-major, so nothing is transposed;
 //   - one warp issues the MMAs into a ring of accumulators in tensor memory;
-//   - epilogue warps add the accumulators up in registers and apply the epilogue:
-//     through a swizzled patch of shared memory per warp, so that global loads and
-//     stores run along the rows.
+//   - epilogue warps add the accumulators up in registers and apply the epilogue.
 // Float32 operands are split by truncation into three bfloat16 parts x = x0 + x1 + x2
 // (8 bits each: exact), and a product is the sum of the six part products x0 w0, x0 w1,
 // x1 w0, x1 w1, x0 w2, x2 w0: what is left out is below 2^-22 of it. That is as many
@@ -39,16 +37,29 @@ namespace {
 enum class Product { kForward, kGradX, kGradW };
 
 constexpr int kRowsTile = 128, kStageK = 64;
-constexpr int kEpiWarps = 8, kLoadWarps = 8;
-constexpr int kLoaders = 32 * kLoadWarps;
-constexpr int kMmaWarp = kEpiWarps + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+// Warps: 8 of the epilogue, the loaders, one for the MMAs. Four loader warps leave 128
+// registers a thread (13 warps) for the epilogue's sums and the loads in flight; the
+// backward products, whose loaders have dz to compute and whose epilogue is plain, have
+// eight (17 warps, 96).
+constexpr int kEpiWarps = 8;
+template <Product P>
+struct Warps {
+    static constexpr int kLoad = P == Product::kForward ? 4 : 8;
+    static constexpr int kLoaders = 32 * kLoad;
+    static constexpr int kMma = kEpiWarps + kLoad;
+    static constexpr int kThreads = 32 * (kMma + 1);
+};
+constexpr int kBiasRows = Warps<Product::kGradW>::kLoad;  // partial sums of dz per range: one per loader warp
 constexpr int kWaitLimit = 1 << 22;
 constexpr int kRing = 4;               // accumulators in tensor memory
-constexpr int kStageBytes = 32 * 32 * 4;  // epilogue patch of a warp
 constexpr uint32_t kSmemMost = 232448;
 
 __device__ int g_fault;
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
 
 template <typename T>
 constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
@@ -56,7 +67,7 @@ constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 template <typename T>
 constexpr int kChunk = sizeof(T) == 4 ? 1 : 16;
 
-// Shared memory of one instance: `stages` slots of A and B parts, the epilogue patches, barriers.
+// Shared memory of one instance: slots of A and B parts, barriers.
 template <typename T, Product P, int BN>
 struct Layout {
     static constexpr bool kAMn = P == Product::kGradW;   // A is MN-major (contraction over rows)
@@ -64,12 +75,11 @@ struct Layout {
     static constexpr uint32_t kAPart = kRowsTile * kStageK * 2;
     static constexpr uint32_t kBPart = kBMn && BN < 64 ? 64u * kStageK * 2 : (uint32_t)BN * kStageK * 2;
     static constexpr uint32_t kSlot = kParts<T> * (kAPart + kBPart);
-    static constexpr uint32_t kTail = kEpiWarps * kStageBytes + 256;
+    static constexpr uint32_t kTail = 256;  // barriers
     static constexpr int kFit = (int)((kSmemMost - kTail) / kSlot);
-    static constexpr int kSlots = kFit < 4 ? kFit : 4;
-    static constexpr uint32_t kOffStage = kSlots * kSlot;
-    static constexpr uint32_t kOffBars = kOffStage + kEpiWarps * kStageBytes;
-    static constexpr uint32_t kBytes = kOffStage + kTail;
+    static constexpr int kSlots = kFit < 6 ? kFit : 6;
+    static constexpr uint32_t kOffBars = kSlots * kSlot;
+    static constexpr uint32_t kBytes = kOffBars + kTail;
     static constexpr uint32_t kTmemCols = kRing * BN;
     static_assert(kSlots >= 2 && kBytes <= kSmemMost && kTmemCols <= 512, "linear layer shared memory");
 };
@@ -91,38 +101,68 @@ struct Job {
     RowMap map;               // rows of the output operands
     Rows out, z, residual;
     const void* bias = nullptr;
-    int vec_out = 0, vec_z = 0, vec_res = 0;
+    int vec_out = 0;  // the epilogue's operands move 2 elements at a time
     void* gW = nullptr;
     float *part = nullptr, *bias_part = nullptr;
+    const unsigned char* image = nullptr;  // B as tiles of operand parts, or null
 };
 
-__device__ __forceinline__ uint4 ldg16(const void* p) {
+// Loads under a predicate, zeros where it is false. The predicate is inside the
+// instruction: a branch around a load would make the warp wait for it at the join.
+__device__ __forceinline__ uint4 ldg16(const void* p, bool on) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile(
+        "{\n .reg .pred pp;\n setp.ne.b32 pp, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
+        " mov.u32 %3, 0;\n @pp ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)on));
+    return v;
+}
+__device__ __forceinline__ uint32_t ldg_elem(const float* p, bool on) {
+    uint32_t v;
+    asm volatile("{\n .reg .pred pp;\n setp.ne.b32 pp, %2, 0;\n mov.u32 %0, 0;\n @pp ld.global.nc.u32 %0, [%1];\n}"
+                 : "=&r"(v)
+                 : "l"(p), "r"((int)on));
+    return v;
+}
+__device__ __forceinline__ uint32_t ldg_elem(const __nv_bfloat16* p, bool on) {
+    uint32_t v;
+    asm volatile(
+        "{\n .reg .pred pp;\n .reg .u16 h;\n setp.ne.b32 pp, %2, 0;\n mov.u16 h, 0;\n @pp ld.global.nc.u16 h, [%1];\n"
+        " cvt.u32.u16 %0, h;\n}"
+        : "=&r"(v)
+        : "l"(p), "r"((int)on));
     return v;
 }
 
-// Eight consecutive elements of a row as they lie in memory, zeros past ncols.
+// 16 bytes of global memory into shared memory asynchronously, zeros where `on` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Eight consecutive elements of a row as they lie in memory, zeros past the `left` that remain.
 template <typename T>
 struct Unit;
 template <>
 struct Unit<float> {
     uint4 a, b;
-    __device__ __forceinline__ void clear() { a = b = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const float* p, int left, bool vec) {
-        clear();
-        if (vec) {
-            if (left >= 4) a = ldg16(p);
-            if (left >= 8) b = ldg16(p + 4);
-            return;
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float* p, int left) {
+        if constexpr (VEC) {
+            a = ldg16(p, left >= 4);
+            b = ldg16(p + 4, left >= 8);
+        } else {
+            a = make_uint4(ldg_elem(p, left > 0), ldg_elem(p + 1, left > 1), ldg_elem(p + 2, left > 2),
+                           ldg_elem(p + 3, left > 3));
+            b = make_uint4(ldg_elem(p + 4, left > 4), ldg_elem(p + 5, left > 5), ldg_elem(p + 6, left > 6),
+                           ldg_elem(p + 7, left > 7));
         }
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < left ? __float_as_uint(__ldg(p + j)) : 0u;
-        a = make_uint4(v[0], v[1], v[2], v[3]);
-        b = make_uint4(v[4], v[5], v[6], v[7]);
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z);
@@ -133,18 +173,16 @@ struct Unit<float> {
 template <>
 struct Unit<__nv_bfloat16> {
     uint4 a;
-    __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, int left, bool vec) {
-        clear();
-        if (vec) {
-            if (left >= 8) a = ldg16(p);
-            return;
+    template <bool VEC>
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int left) {
+        if constexpr (VEC) {
+            a = ldg16(p, left >= 8);
+        } else {
+            a = make_uint4(ldg_elem(p, left > 0) | ldg_elem(p + 1, left > 1) << 16,
+                           ldg_elem(p + 2, left > 2) | ldg_elem(p + 3, left > 3) << 16,
+                           ldg_elem(p + 4, left > 4) | ldg_elem(p + 5, left > 5) << 16,
+                           ldg_elem(p + 6, left > 6) | ldg_elem(p + 7, left > 7) << 16);
         }
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = j < left ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + j) : 0u;
-        a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
@@ -172,7 +210,11 @@ __device__ __forceinline__ void store_parts(unsigned char* dst, uint32_t part, f
                                                                    high_pair(v[4], v[5]), high_pair(v[6], v[7]));
             if (p < 2)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] -= high_part(v[j]);
+                for (int j = 0; j < 8; j += 2) {  // packed: v - high_part(v)
+                    const float2 r = __fadd2_rn(make_float2(v[j], v[j + 1]),
+                                                make_float2(-high_part(v[j]), -high_part(v[j + 1])));
+                    v[j] = r.x, v[j + 1] = r.y;
+                }
         }
     }
 }
@@ -202,40 +244,59 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t da, uint64_t db, u
         : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p, int left, bool vec) {
-    if constexpr (sizeof(T) == 4) {
-        if (vec) return *reinterpret_cast<const float4*>(p);
-    } else {
-        if (vec) {
-            const uint2 q = *reinterpret_cast<const uint2*>(p);
-            return make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
-        }
-    }
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    v.x = to_float(p[0]);
-    if (left > 1) v.y = to_float(p[1]);
-    if (left > 2) v.z = to_float(p[2]);
-    if (left > 3) v.w = to_float(p[3]);
-    return v;
+// Two elements of a row, zeros past the `left` that remain. V: both at once (they are
+// aligned and `left` is not 1). The statements are volatile, so that they stay in order:
+// a residual that is the output is read before it is written, and one row at a time.
+template <bool V>
+__device__ __forceinline__ float2 load2(const float* p, int left) {
+    float a, b;
+    if constexpr (V)
+        asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %3, 0;\n mov.f32 %0, 0f00000000;\n mov.f32 %1, 0f00000000;\n"
+            " @pp ld.global.v2.f32 {%0, %1}, [%2];\n}"
+            : "=&f"(a), "=&f"(b)
+            : "l"(p), "r"(left));
+    else
+        asm volatile("{\n .reg .pred p0, p1;\n setp.gt.s32 p0, %3, 0;\n setp.gt.s32 p1, %3, 1;\n mov.f32 %0, 0f00000000;\n"
+            " mov.f32 %1, 0f00000000;\n @p0 ld.global.f32 %0, [%2];\n @p1 ld.global.f32 %1, [%2+4];\n}"
+            : "=&f"(a), "=&f"(b)
+            : "l"(p), "r"(left));
+    return make_float2(a, b);
 }
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 v, int left, bool vec) {
-    if constexpr (sizeof(T) == 4) {
-        if (vec) {
-            *reinterpret_cast<float4*>(p) = v;
-            return;
-        }
-    } else {
-        if (vec) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-            return;
-        }
-    }
-    p[0] = from_float<T>(v.x);
-    if (left > 1) p[1] = from_float<T>(v.y);
-    if (left > 2) p[2] = from_float<T>(v.z);
-    if (left > 3) p[3] = from_float<T>(v.w);
+template <bool V>
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p, int left) {
+    uint32_t a;
+    if constexpr (V)
+        asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %2, 0;\n mov.u32 %0, 0;\n @pp ld.global.u32 %0, [%1];\n}"
+            : "=&r"(a)
+            : "l"(p), "r"(left));
+    else
+        asm volatile("{\n .reg .pred p0, p1;\n .reg .u16 h0, h1;\n setp.gt.s32 p0, %2, 0;\n setp.gt.s32 p1, %2, 1;\n"
+            " mov.u16 h0, 0;\n mov.u16 h1, 0;\n @p0 ld.global.u16 h0, [%1];\n @p1 ld.global.u16 h1, [%1+2];\n"
+            " mov.b32 %0, {h0, h1};\n}"
+            : "=&r"(a)
+            : "l"(p), "r"(left));
+    return make_float2(bf16_lo(a), bf16_hi(a));
+}
+template <bool V>
+__device__ __forceinline__ void store2(float* p, float2 v, int left) {
+    if constexpr (V)
+        asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %3, 0;\n @pp st.global.v2.f32 [%0], {%1, %2};\n}" ::"l"(p),
+                     "f"(v.x), "f"(v.y), "r"(left));
+    else
+        asm volatile("{\n .reg .pred p0, p1;\n setp.gt.s32 p0, %3, 0;\n setp.gt.s32 p1, %3, 1;\n"
+                     " @p0 st.global.f32 [%0], %1;\n @p1 st.global.f32 [%0+4], %2;\n}" ::"l"(p),
+                     "f"(v.x), "f"(v.y), "r"(left));
+}
+template <bool V>
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v, int left) {
+    const uint32_t a = pack_bf16(v.x, v.y);
+    if constexpr (V)
+        asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %2, 0;\n @pp st.global.u32 [%0], %1;\n}" ::"l"(p), "r"(a),
+                     "r"(left));
+    else
+        asm volatile("{\n .reg .pred p0, p1;\n .reg .u16 h0, h1;\n setp.gt.s32 p0, %2, 0;\n setp.gt.s32 p1, %2, 1;\n"
+                     " mov.b32 {h0, h1}, %1;\n @p0 st.global.u16 [%0], h0;\n @p1 st.global.u16 [%0+2], h1;\n}" ::"l"(p),
+                     "r"(a), "r"(left));
 }
 
 // One work item: an output tile, and the range of the contraction it covers.
@@ -260,9 +321,68 @@ __device__ __forceinline__ Item item_of(const Job& j, int i, int bn) {
     return it;
 }
 
+// The epilogue of a tile on one warp's 32 rows x BN / 2 columns, in the accumulator's
+// fragment layout: a lane holds 4 rows, of each 2 neighbouring columns in every 8. The 4
+// lanes of a row make whole 32-byte sectors of float32, so loads and stores go straight
+// between registers and memory, and a lane has 4 row addresses, not one per element.
+// V: every operand of the epilogue moves 2 elements at a time.
+template <typename T, Product P, int BN, bool V>
+__device__ __forceinline__ void finish(const Job& job, const Item& it, float (&acc)[2][BN / 4], int quad, int half,
+                                       int lane) {
+    constexpr int kGroups = BN / 16;  // groups of 8 columns
+    const int n0 = it.n0 + half * (BN / 2) + 2 * (lane & 3);
+    const bool has_res = P == Product::kForward && job.residual.p != nullptr;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int m = it.m0 + quad * 32 + 8 * r + (lane >> 2);
+        const int left = m < job.m ? job.n - n0 : 0;
+        float2 v[kGroups];
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c)
+            v[c] = make_float2(acc[r >> 1][4 * c + 2 * (r & 1)], acc[r >> 1][4 * c + 2 * (r & 1) + 1]);
+        if constexpr (P == Product::kForward) {
+            float2 res[kGroups];
+            if (has_res) {
+                const T* p = static_cast<const T*>(job.residual.p) + job.residual.offset(job.map, m) + n0;
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) res[c] = load2<V>(p + 8 * c, left - 8 * c);
+            }
+            if (job.bias) {
+                const T* p = static_cast<const T*>(job.bias) + n0;
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) {
+                    const float2 b = load2<V>(p + 8 * c, job.n - n0 - 8 * c);
+                    v[c].x += b.x, v[c].y += b.y;
+                }
+            }
+            if (job.z.p) {
+                T* p = static_cast<T*>(job.z.p) + job.z.offset(job.map, m) + n0;
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
+            }
+            if (job.silu)
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) v[c].x = silu(v[c].x), v[c].y = silu(v[c].y);
+            if (has_res)
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) v[c].x += res[c].x, v[c].y += res[c].y;
+        }
+        if (P == Product::kGradW && job.part) {
+            float* p = job.part + ((size_t)it.split * job.m + m) * job.n + n0;
+#pragma unroll
+            for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
+        } else {
+            T* p = P == Product::kGradW ? static_cast<T*>(job.gW) + (size_t)m * job.n + n0
+                                        : static_cast<T*>(job.out.p) + job.out.offset(job.map, m) + n0;
+#pragma unroll
+            for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
+        }
+    }
+}
+
 // A loader's share of an operand tile of ROWS source rows by COLS columns: units of 8
 // columns, unit u = t + 256 i at row u / (COLS / 8).
-template <int ROWS, int COLS>
+template <int ROWS, int COLS, int kLoaders>
 struct Share {
     static constexpr int kPerRow = COLS / 8;
     static constexpr int kIters = ROWS * kPerRow / kLoaders;
@@ -276,23 +396,31 @@ struct Share {
     }
 };
 
-template <typename T, Product P, int BN>
-__global__ void __launch_bounds__(kThreads, 1) etp_linear_kernel(const __grid_constant__ Job job) {
+// IMAGE: B arrives as ready tiles (etp_linear_image_kernel) by bulk copies.
+template <typename T, Product P, int BN, bool VEC, bool IMAGE>
+__global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const __grid_constant__ Job job) {
     using Lay = Layout<T, P, BN>;
     constexpr int NP = kParts<T>;
+    constexpr int kLoadWarps = Warps<P>::kLoad, kLoaders = Warps<P>::kLoaders, kMmaWarp = Warps<P>::kMma;
     constexpr bool kDzA = P == Product::kGradX, kDzB = P == Product::kGradW;
-    // what a loader holds in flight: whole shares, or halves of them beside the pre-activation
-    constexpr int kHalves = P == Product::kForward ? 1 : 2;
-    using ShareA = Share<Lay::kAMn ? kStageK : kRowsTile, Lay::kAMn ? kRowsTile : kStageK>;
-    using ShareB = Share<Lay::kBMn ? kStageK : BN, Lay::kBMn ? BN : kStageK>;
+    // bfloat16 operands that need no arithmetic are copied straight to shared memory
+    constexpr bool kCopyA = sizeof(T) == 2 && VEC && !kDzA, kCopyB = sizeof(T) == 2 && VEC && !kDzB && !IMAGE;
+    constexpr bool kCopies = kCopyA || kCopyB;
+    constexpr bool kRegA = !kCopyA, kRegB = !kCopyB && !IMAGE;
+    constexpr int kDepth = Lay::kSlots - 1;  // stages of copies in flight
+    // parts of a stage that a loader holds in flight in turn, as registers allow
+    constexpr int kHalves = IMAGE || sizeof(T) == 2 ? (P == Product::kForward ? 1 : 2) : P == Product::kGradX ? 4 : 2;
+    using ShareA = Share<Lay::kAMn ? kStageK : kRowsTile, Lay::kAMn ? kRowsTile : kStageK, kLoaders>;
+    using ShareB = Share<Lay::kBMn ? kStageK : BN, Lay::kBMn ? BN : kStageK, kLoaders>;
     constexpr int IA = ShareA::kIters, IB = ShareB::kIters;
-    constexpr int HA = (IA + kHalves - 1) / kHalves, HB = (IB + kHalves - 1) / kHalves;
+    constexpr int HA = (IA + kHalves - 1) / kHalves, HB = (IB + kHalves - 1) / kHalves;  // units of a part
 
     extern __shared__ __align__(1024) unsigned char smem[];
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBars);
-    uint64_t* empty = full + Lay::kSlots;
-    uint64_t* tfull = empty + Lay::kSlots;
-    uint64_t* tempty = tfull + kRing;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBars);  // a slot's operands are written
+    uint64_t* bfull = full + Lay::kSlots;                                 // its image tile has arrived
+    uint64_t* empty = bfull + Lay::kSlots;                                // its MMAs are done
+    uint64_t* tfull = empty + Lay::kSlots;                                // an accumulator is complete
+    uint64_t* tempty = tfull + kRing;                                     // and has been read
     uint64_t* drain = tempty + kRing;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -302,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) etp_linear_kernel(const __grid_co
     if (t == 0) {
         for (int i = 0; i < Lay::kSlots; ++i) {
             tc::mbar_init(&full[i], kLoadWarps);
+            tc::mbar_init(&bfull[i], 1);
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -316,49 +445,85 @@ __global__ void __launch_bounds__(kThreads, 1) etp_linear_kernel(const __grid_co
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    // A bounded wait, the same answer for the whole warp; false: leave the loops.
-    auto wait = [&](uint64_t* bar, unsigned parity) {
+    // A bounded wait; false: leave the loops. wait(): the same answer for the whole warp.
+    auto wait1 = [&](uint64_t* bar, unsigned parity) {
         const bool ok = !*abort_flag && tc::mbar_wait(bar, parity, kWaitLimit);
         if (!ok) *abort_flag = 1;
-        return __all_sync(0xffffffffu, ok) != 0;
+        return ok;
     };
+    auto wait = [&](uint64_t* bar, unsigned parity) { return __all_sync(0xffffffffu, wait1(bar, parity)) != 0; };
+    int images = 0;  // (loader thread 0) image tiles asked for
 
     if (warp >= kEpiWarps && warp < kMmaWarp) {  // loaders
         const int lt = t - 32 * kEpiWarps;
-        Unit<T> ra[HA], rb[HB], rz[kDzA ? HA : kDzB ? HB : 1];
-        auto load_a = [&](const Item& it, int ks, int h) {
-            const int kk = it.k0 + ks * kStageK;
-            const int row0 = Lay::kAMn ? kk : it.m0, col0 = Lay::kAMn ? it.m0 : kk;
-            const int rlim = Lay::kAMn ? it.k1 : job.A.nrows;
-            const int c = col0 + 8 * ShareA::col(lt), left = job.A.ncols - c;
+        Unit<T> ra[kRegA ? HA : 1], rb[kRegB ? HB : 1], rz[kDzA ? HA : kDzB ? HB : 1];
+        // Two cursors: the stage that is stored now, and the one that is fetched into registers.
+        struct Cursor {
+            int i, ks;
+            Item it;
+        } now{(int)blockIdx.x, 0, item_of<P>(job, blockIdx.x, BN)}, next = now;
+        auto advance = [&](Cursor& c) {  // true: another item
+            if (++c.ks < c.it.stages) return false;
+            c.ks = 0;
+            c.i += gridDim.x;
+            if (c.i >= job.items) return false;
+            c.it = item_of<P>(job, c.i, BN);
+            return true;
+        };
+        // addresses of a K-major A's rows, for the cursor that reads it
+        const T *arow[Lay::kAMn ? 1 : IA], *zrow[kDzA ? IA : 1];
+        auto set_rows = [&](const Item& it) {
+            if constexpr (!Lay::kAMn) {
 #pragma unroll
-            for (int i = 0; i < HA; ++i) {
-                const int r = row0 + ShareA::row(lt, h * HA + i);
-                ra[i].clear();
-                if (kDzA) rz[i].clear();
-                if (h * HA + i < IA && r < rlim && left > 0) {
-                    ra[i].load(static_cast<const T*>(job.A.rows.p) + job.A.rows.offset(job.A.map, r) + c, left, job.A.vec);
-                    if (kDzA && job.silu)
-                        rz[i].load(static_cast<const T*>(job.Z.rows.p) + job.Z.rows.offset(job.Z.map, r) + c, left,
-                                   job.Z.vec);
+                for (int i = 0; i < IA; ++i) {
+                    const int r = it.m0 + ShareA::row(lt, i);
+                    arow[i] = static_cast<const T*>(job.A.rows.p) + job.A.rows.offset(job.A.map, r) + 8 * ShareA::col(lt);
+                    if constexpr (kDzA) {
+                        zrow[i] =
+                            static_cast<const T*>(job.Z.rows.p) + job.Z.rows.offset(job.Z.map, r) + 8 * ShareA::col(lt);
+                    }
                 }
             }
         };
-        auto load_b = [&](const Item& it, int ks, int h) {
-            const int kk = it.k0 + ks * kStageK;
-            const int row0 = Lay::kBMn ? kk : it.n0, col0 = Lay::kBMn ? it.n0 : kk;
-            const int rlim = kDzB ? it.k1 : job.B.nrows;
-            const int c = col0 + 8 * ShareB::col(lt), left = job.B.ncols - c;
-#pragma unroll
-            for (int i = 0; i < HB; ++i) {
-                const int r = row0 + ShareB::row(lt, h * HB + i);
-                rb[i].clear();
-                if (kDzB) rz[i].clear();
-                if (h * HB + i < IB && r < rlim && left > 0) {
-                    rb[i].load(static_cast<const T*>(job.B.rows.p) + job.B.rows.offset(job.B.map, r) + c, left, job.B.vec);
-                    if (kDzB && job.silu)
-                        rz[i].load(static_cast<const T*>(job.Z.rows.p) + job.Z.rows.offset(job.Z.map, r) + c, left,
-                                   job.Z.vec);
+        // unit i of a stage's A (B) tile: its address, and how many of its elements exist
+        auto unit_a = [&](const Cursor& c, int i, const T*& p) {
+            const int kk = c.it.k0 + c.ks * kStageK;
+            if constexpr (Lay::kAMn) {
+                const int r = kk + ShareA::row(lt, i), col = c.it.m0 + 8 * ShareA::col(lt);
+                p = static_cast<const T*>(job.A.rows.p) + job.A.rows.offset(job.A.map, r) + col;
+                return r < c.it.k1 ? job.A.ncols - col : 0;
+            } else {
+                p = arow[i] + kk;
+                return c.it.m0 + ShareA::row(lt, i) < job.A.nrows ? job.A.ncols - kk - 8 * ShareA::col(lt) : 0;
+            }
+        };
+        auto unit_b = [&](const Cursor& c, int i, const T*& p, const T*& pz) {
+            const int kk = c.it.k0 + c.ks * kStageK;
+            const int r = (Lay::kBMn ? kk : c.it.n0) + ShareB::row(lt, i);
+            const int col = (Lay::kBMn ? c.it.n0 : kk) + 8 * ShareB::col(lt);
+            p = static_cast<const T*>(job.B.rows.p) + job.B.rows.offset(job.B.map, r) + col;
+            if (kDzB) pz = static_cast<const T*>(job.Z.rows.p) + job.Z.rows.offset(job.Z.map, r) + col;
+            return r < (kDzB ? c.it.k1 : job.B.nrows) ? job.B.ncols - col : 0;
+        };
+        auto fetch_a = [&](const Cursor& c, int h, int q) {  // unit q of part h (and its pre-activation)
+            if constexpr (kRegA) {
+                if (h * HA + q >= IA) return;
+                const T* p;
+                const int left = unit_a(c, h * HA + q, p);
+                ra[q].template load<VEC>(p, left);
+                if constexpr (kDzA) {
+                    if (job.silu) rz[q].template load<VEC>(zrow[h * HA + q] + c.it.k0 + c.ks * kStageK, left);
+                }
+            }
+        };
+        auto fetch_b = [&](const Cursor& c, int h, int q) {
+            if constexpr (kRegB) {
+                if (h * HB + q >= IB) return;
+                const T *p, *pz = nullptr;
+                const int left = unit_b(c, h * HB + q, p, pz);
+                rb[q].template load<VEC>(p, left);
+                if constexpr (kDzB) {
+                    if (job.silu) rz[q].template load<VEC>(pz, left);
                 }
             }
         };
@@ -369,83 +534,139 @@ __global__ void __launch_bounds__(kThreads, 1) etp_linear_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= silu_grad(zv[j]);
         };
+        auto arrive = [&](int slot) {  // this warp's part of the slot is written
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&full[slot]);
+        };
         float bsum[8];
-        int i = blockIdx.x, ks = 0;
-        Item it = item_of<P>(job, i, BN);
-        load_a(it, 0, 0);
-        load_b(it, 0, 0);
-        for (int n = 0; i < job.items; ++n) {
+        int n = 0;
+        set_rows(now.it);
+#pragma unroll
+        for (int q = 0; q < HA; ++q) fetch_a(now, 0, q);
+#pragma unroll
+        for (int q = 0; q < HB; ++q) fetch_b(now, 0, q);
+        for (; now.i < job.items; ++n) {
             const int slot = n % Lay::kSlots;
             if (n >= Lay::kSlots && !wait(&empty[slot], (n / Lay::kSlots - 1) & 1)) break;
             unsigned char* sa = smem + slot * Lay::kSlot;
             unsigned char* sb = sa + NP * Lay::kAPart;
-            if (kDzB && ks == 0)
+            if (IMAGE && lt == 0) {
+                const int nks = (job.k + kStageK - 1) / kStageK;
+                tc::mbar_expect_tx(&bfull[slot], NP * Lay::kBPart);
+                tc::bulk_g2s(sb, job.image + (size_t)((now.it.n0 / BN) * nks + now.ks) * (NP * Lay::kBPart),
+                             NP * Lay::kBPart, &bfull[slot]);
+                images = n + 1;
+            }
+            if constexpr (kCopyA) {
+#pragma unroll
+                for (int q = 0; q < IA; ++q) {
+                    const T* p;
+                    const int left = unit_a(now, q, p);
+                    copy16(sa + ShareA::offset(lt, q), left > 0 ? p : static_cast<const T*>(job.A.rows.p), left > 0);
+                }
+            }
+            if constexpr (kCopyB) {
+#pragma unroll
+                for (int q = 0; q < IB; ++q) {
+                    const T *p, *pz = nullptr;
+                    const int left = unit_b(now, q, p, pz);
+                    copy16(sb + ShareB::offset(lt, q), left > 0 ? p : static_cast<const T*>(job.B.rows.p), left > 0);
+                }
+            }
+            if (kCopies) copy_commit();
+            if (kDzB && now.ks == 0)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) bsum[j] = 0.f;
-            // the stage after this one
-            int ni = i, nks = ks + 1;
-            Item nit = it;
-            if (nks >= it.stages) {
-                nks = 0;
-                ni = i + gridDim.x;
-                if (ni < job.items) nit = item_of<P>(job, ni, BN);
-            }
-            const bool more = ni < job.items;
+            // a unit's registers are refilled as soon as it is stored: it is in flight while the others are converted
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
+                const bool here = h + 1 < kHalves;
+                if (!here && advance(next) && kRegA) set_rows(next.it);
+                const bool more = next.i < job.items;
+                if constexpr (kRegA) {
 #pragma unroll
-                for (int q = 0; q < HA; ++q)
-                    if (h * HA + q < IA) {
-                        float v[8];
-                        ra[q].get(v);
-                        if (kDzA) dz(v, rz[q]);
-                        store_parts<T>(sa + ShareA::offset(lt, h * HA + q), Lay::kAPart, v);
-                    }
-                if (h + 1 < kHalves)
-                    load_a(it, ks, h + 1);
-                else if (more)
-                    load_a(nit, nks, 0);
-#pragma unroll
-                for (int q = 0; q < HB; ++q)
-                    if (h * HB + q < IB) {
-                        float v[8];
-                        rb[q].get(v);
-                        if (kDzB) {
-                            dz(v, rz[q]);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) bsum[j] += v[j];
+                    for (int q = 0; q < HA; ++q) {
+                        if (h * HA + q < IA) {
+                            float v[8];
+                            ra[q].get(v);
+                            if constexpr (kDzA) {
+                                dz(v, rz[q]);
+                            }
+                            store_parts<T>(sa + ShareA::offset(lt, h * HA + q), Lay::kAPart, v);
                         }
-                        store_parts<T>(sb + ShareB::offset(lt, h * HB + q), Lay::kBPart, v);
+                        if (here)
+                            fetch_a(now, h + 1, q);
+                        else if (more)
+                            fetch_a(next, 0, q);
                     }
-                if (h + 1 < kHalves)
-                    load_b(it, ks, h + 1);
-                else if (more)
-                    load_b(nit, nks, 0);
+                }
+                if constexpr (kRegB) {
+#pragma unroll
+                    for (int q = 0; q < HB; ++q) {
+                        if (h * HB + q < IB) {
+                            float v[8];
+                            rb[q].get(v);
+                            if constexpr (kDzB) {
+                                dz(v, rz[q]);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) bsum[j] += v[j];
+                            }
+                            store_parts<T>(sb + ShareB::offset(lt, h * HB + q), Lay::kBPart, v);
+                        }
+                        if (here)
+                            fetch_b(now, h + 1, q);
+                        else if (more)
+                            fetch_b(next, 0, q);
+                    }
+                }
             }
-            tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&full[slot]);
-            if (kDzB && ks + 1 >= it.stages && job.bias_part && it.m0 == 0) {
+            if (!kCopies) {
+                arrive(slot);
+            } else if (n >= kDepth) {
+                copy_wait<kDepth>();
+                arrive((n - kDepth) % Lay::kSlots);
+            }
+            if (kDzB && now.ks + 1 >= now.it.stages && job.bias_part && now.it.m0 == 0) {
                 // the item's sums of dz over its rows: the lanes of a warp that share columns, one row per warp
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     for (int o = ShareB::kPerRow; o < 32; o <<= 1) bsum[j] += __shfl_xor_sync(0xffffffffu, bsum[j], o);
                 if (lane < ShareB::kPerRow) {
-                    float* row = job.bias_part + (size_t)(it.split * kLoadWarps + (warp - kEpiWarps)) * job.n;
+                    float* row = job.bias_part + (size_t)(now.it.split * kLoadWarps + (warp - kEpiWarps)) * job.n;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int c = it.n0 + 8 * ShareB::col(lt) + j;
+                        const int c = now.it.n0 + 8 * ShareB::col(lt) + j;
                         if (c < job.n) row[c] = bsum[j];
                     }
                 }
             }
-            i = ni, ks = nks, it = nit;
+            now = next;
+            if (kCopyA && now.ks == 0) set_rows(now.it);
         }
-    } else if (warp == kMmaWarp) {
+        if (kCopies) {
+            copy_wait<0>();
+            for (int m = n > kDepth ? n - kDepth : 0; m < n; ++m) arrive(m % Lay::kSlots);
+        }
+    } else if (warp == kMmaWarp && lane == 0) {
         constexpr uint32_t idesc = idesc_bf16<Lay::kAMn, Lay::kBMn>(BN);
-        constexpr uint32_t kStepA = Lay::kAMn ? 2048 : 32, kStepB = Lay::kBMn ? 2048 : 32;  // 16 k
+        // one K step of 16, one part: descriptor units of 16 bytes
+        constexpr uint32_t kStepA = (Lay::kAMn ? 2048 : 32) >> 4, kStepB = (Lay::kBMn ? 2048 : 32) >> 4;
         constexpr int kPairs = NP == 3 ? 6 : 1;
         constexpr int pa[6] = {NP == 3 ? 1 : 0, 0, 2, 0, 1, 0}, pb[6] = {NP == 3 ? 1 : 0, 2, 0, 1, 0, 0};
+        const uint64_t base_a = desc128<Lay::kAMn>(tc::smem_u32(smem));
+        const uint64_t base_b = desc128<Lay::kBMn>(tc::smem_u32(smem + NP * Lay::kAPart));
+        // the stage's MMAs, unrolled: descriptors are the slot's plus constants
+        auto issue = [&](auto steps_c, uint32_t d, uint64_t da, uint64_t db, bool first) {
+            constexpr int S = decltype(steps_c)::value;
+#pragma unroll
+            for (int q = 0; q < kPairs; ++q)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    mma_bf16(d, da + (uint64_t)(pa[q] * (Lay::kAPart >> 4) + s * kStepA),
+                             db + (uint64_t)(pb[q] * (Lay::kBPart >> 4) + s * kStepB), idesc,
+                             q == 0 && s == 0 ? (first ? 0u : 1u) : 1u);
+        };
         int n = 0, chunk = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
@@ -453,48 +674,40 @@ __global__ void __launch_bounds__(kThreads, 1) etp_linear_kernel(const __grid_co
             for (int ks = 0; ks < it.stages; ++ks, ++n) {
                 const int slot = n % Lay::kSlots, buf = chunk % kRing;
                 const bool first = ks % kChunk<T> == 0;
-                if (first && chunk >= kRing && !wait(&tempty[buf], (chunk / kRing - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                if (!wait(&full[slot], (n / Lay::kSlots) & 1)) {
+                if ((first && chunk >= kRing && !wait1(&tempty[buf], (chunk / kRing - 1) & 1)) ||
+                    !wait1(&full[slot], (n / Lay::kSlots) & 1) ||
+                    (IMAGE && !wait1(&bfull[slot], (n / Lay::kSlots) & 1))) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
                 const int left = it.k1 - it.k0 - ks * kStageK;
-                const int steps = left >= kStageK ? kStageK / 16 : (left + 15) / 16;
-                const bool last = ks + 1 == it.stages || (ks + 1) % kChunk<T> == 0;
-                if (lane == 0) {
-                    const uint32_t sa = tc::smem_u32(smem + slot * Lay::kSlot), sb = sa + NP * Lay::kAPart;
-#pragma unroll
-                    for (int q = 0; q < kPairs; ++q)
-                        for (int s = 0; s < steps; ++s)
-                            mma_bf16(tmem + buf * BN, desc128<Lay::kAMn>(sa + pa[q] * Lay::kAPart + s * kStepA),
-                                     desc128<Lay::kBMn>(sb + pb[q] * Lay::kBPart + s * kStepB), idesc,
-                                     first && q == 0 && s == 0 ? 0u : 1u);
-                    tc::mma_commit(&empty[slot]);
-                    if (last) tc::mma_commit(&tfull[buf]);
+                const uint32_t d = tmem + buf * BN;
+                const uint64_t da = base_a + (uint64_t)(slot * (Lay::kSlot >> 4));
+                const uint64_t db = base_b + (uint64_t)(slot * (Lay::kSlot >> 4));
+                if (left > 48) issue(Int<4>{}, d, da, db, first);
+                else if (left > 32) issue(Int<3>{}, d, da, db, first);
+                else if (left > 16) issue(Int<2>{}, d, da, db, first);
+                else issue(Int<1>{}, d, da, db, first);
+                tc::mma_commit(&empty[slot]);
+                if (ks + 1 == it.stages || (ks + 1) % kChunk<T> == 0) {
+                    tc::mma_commit(&tfull[buf]);
+                    ++chunk;
                 }
-                __syncwarp();
-                if (last) ++chunk;
             }
         }
-    } else {  // epilogue
-        constexpr int NC = BN / 2;                  // columns of a warp
-        constexpr int CW = NC < 32 ? NC : 32;       // columns at a time
-        constexpr int LPR = CW / 4, RPI = 32 / LPR;  // lanes per row, rows per pass
+    } else if (warp < kEpiWarps) {
+        constexpr int NR = BN / 4;  // registers of a warp's 16 lanes x BN / 2 columns
+        constexpr int kPiece = NR < 16 ? NR : 16;
         const int quad = warp & 3, half = warp >> 2;
-        float* st = reinterpret_cast<float*>(smem + Lay::kOffStage + warp * kStageBytes);
-        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + half * NC;
-        auto swz = [](int row, int j) { return LPR == 8 ? (j ^ (row & 7)) : (j ^ ((row >> 1) & 3)); };
+        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
         int chunk = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
             const Item it = item_of<P>(job, i, BN);
-            float acc[NC];
+            float acc[2][NR];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+            for (int j = 0; j < NR; ++j) acc[0][j] = acc[1][j] = 0.f;
             for (int ks = 0; ks < it.stages; ks += kChunk<T>, ++chunk) {
                 const int buf = chunk % kRing;
                 if (!wait(&tfull[buf], (chunk / kRing) & 1)) {
@@ -503,71 +716,70 @@ __global__ void __launch_bounds__(kThreads, 1) etp_linear_kernel(const __grid_co
                 }
                 tc::fence_after_sync();
 #pragma unroll
-                for (int c = 0; c < NC; c += 16) {
-                    float v[16];
-                    tc::tmem_ld<16>(lane_base + buf * BN + c, v);
-                    tc::tmem_wait_ld(v);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
-                }
+                    for (int c = 0; c < NR; c += kPiece) {
+                        float v[kPiece];
+                        tc::tmem_ld_frag<kPiece>(base + ((uint32_t)(16 * h) << 16) + buf * BN + 2 * c, v);
+                        tc::tmem_wait_ld(v);
+#pragma unroll
+                        for (int j = 0; j < kPiece; ++j) acc[h][c + j] += v[j];
+                    }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&tempty[buf]);
             }
             if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < NC; c += CW) {
-#pragma unroll
-                for (int j = 0; j < LPR; ++j)
-                    *reinterpret_cast<float4*>(st + lane * CW + 4 * swz(lane, j)) =
-                        make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
-                __syncwarp();
-                const int jj = lane % LPR;
-                const int n = it.n0 + half * NC + c + 4 * jj, left = job.n - n;
-                float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (P == Product::kForward && job.bias && left > 0)
-                    bias = load4(static_cast<const T*>(job.bias) + n, left, false);
-#pragma unroll
-                for (int rr = 0; rr < LPR; ++rr) {
-                    const int row = RPI * rr + lane / LPR, m = it.m0 + quad * 32 + row;
-                    if (m >= job.m || left <= 0) continue;
-                    float4 v = *reinterpret_cast<const float4*>(st + row * CW + 4 * swz(row, jj));
-                    if (P == Product::kForward) {
-                        v.x += bias.x, v.y += bias.y, v.z += bias.z, v.w += bias.w;
-                        if (job.z.p)
-                            store4(static_cast<T*>(job.z.p) + job.z.offset(job.map, m) + n, v, left, job.vec_z);
-                        if (job.silu) v.x = silu(v.x), v.y = silu(v.y), v.z = silu(v.z), v.w = silu(v.w);
-                        if (job.residual.p) {
-                            const float4 r = load4(
-                                static_cast<const T*>(job.residual.p) + job.residual.offset(job.map, m) + n, left,
-                                job.vec_res);
-                            v.x += r.x, v.y += r.y, v.z += r.z, v.w += r.w;
-                        }
-                    }
-                    if (P != Product::kGradW) {
-                        store4(static_cast<T*>(job.out.p) + job.out.offset(job.map, m) + n, v, left, job.vec_out);
-                    } else if (job.part) {
-                        store4(job.part + ((size_t)it.split * job.m + m) * job.n + n, v, left, job.vec_out);
-                    } else {
-                        store4(static_cast<T*>(job.gW) + (size_t)m * job.n + n, v, left, job.vec_out);
-                    }
-                }
-                __syncwarp();
-            }
+            if (job.vec_out)
+                finish<T, P, BN, true>(job, it, acc, quad, half, lane);
+            else
+                finish<T, P, BN, false>(job, it, acc, quad, half, lane);
         }
     }
     __syncthreads();
-    if (*abort_flag) {  // leave no MMA in flight on the freed memory
+    if (*abort_flag) {  // leave no MMA or copy in flight on the freed memory
         if (t == 32 * kMmaWarp) {
             atomicOr(&g_fault, 1);
             tc::mma_commit(drain);
             tc::mbar_wait(drain, 0, kWaitLimit);
         }
+        if (IMAGE && t == 32 * kEpiWarps)
+            for (int m = images > Lay::kSlots ? images - Lay::kSlots : 0; m < images; ++m)
+                tc::mbar_wait(&bfull[m % Lay::kSlots], (m / Lay::kSlots) & 1, kWaitLimit);
         __syncthreads();
     }
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, Lay::kTmemCols);
+}
+
+// W as tiles of operand parts in the layout of a slot's B, tile (nt, ks) after tile:
+// converted once here instead of once per row tile by every CTA. A thread converts
+// units of 8 consecutive elements of W.
+template <typename T, Product P, int BN>
+__global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restrict__ W, int rows, int cols, bool vec,
+                                                               unsigned char* __restrict__ image) {
+    using Lay = Layout<T, P, BN>;
+    constexpr int R = Lay::kBMn ? kStageK : BN, C = Lay::kBMn ? BN : kStageK;  // W's rows and columns in a tile
+    constexpr int kPerRow = C / 8, kUnits = R * kPerRow;
+    const int ct = (cols + C - 1) / C, rt = (rows + R - 1) / R;
+    const int u = blockIdx.x * 256 + threadIdx.x, tile = u / kUnits, w = u % kUnits;
+    if (tile >= ct * rt) return;
+    // tiles along the contraction are adjacent: it runs over W's rows (MN-major) or columns
+    const int rti = Lay::kBMn ? tile % rt : tile / ct, cti = Lay::kBMn ? tile / rt : tile % ct;
+    const int r = w / kPerRow, c = w % kPerRow, gr = rti * R + r, gc = cti * C + 8 * c;
+    const T* p = W + (size_t)gr * cols + gc;
+    const int left = gr < rows ? cols - gc : 0;
+    Unit<T> q;
+    if (vec)
+        q.template load<true>(p, left);
+    else
+        q.template load<false>(p, left);
+    float v[8];
+    q.get(v);
+    store_parts<T>(image + (size_t)tile * kParts<T> * Lay::kBPart + (uint32_t)(c >> 3) * kPanel +
+                       (uint32_t)(r >> 3) * 1024 + (uint32_t)(r & 7) * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4),
+                   Lay::kBPart, v);
 }
 
 // grad_W from the ranges' sums [splits][count] and grad_bias from [bias_rows][N], both in
@@ -597,7 +809,7 @@ __global__ void __launch_bounds__(256)
 }
 
 bool rows_aligned(const Rows& r, int elem, int bytes) {
-    const long long n = bytes / elem;
+    const unsigned n = bytes / elem;
     return (reinterpret_cast<uintptr_t>(r.p) % bytes) == 0 && r.gs % n == 0 && r.rs % n == 0;
 }
 
@@ -610,34 +822,68 @@ Operand operand(const Rows& r, const RowMap& map, int nrows, int ncols, int elem
 
 Operand matrix(const void* p, int nrows, int ncols, int elem) {
     Rows r;
-    r.p = const_cast<void*>(p), r.gs = ncols;
+    r.p = const_cast<void*>(p), r.gs = (unsigned)ncols;
     RowMap map;
     map.M = nrows;
     return operand(r, map, nrows, ncols, elem);
 }
 
-template <typename T, Product P, int BN>
-cudaError_t launch_bn(Job& j, cudaStream_t s) {
+template <typename T, Product P, int BN, bool VEC, bool IMAGE>
+cudaError_t launch_kernel(const Job& j, cudaStream_t s) {
     using Lay = Layout<T, P, BN>;
-    const cudaError_t e = cudaFuncSetAttribute(etp_linear_kernel<T, P, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)Lay::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(etp_linear_kernel<T, P, BN, VEC, IMAGE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kBytes);
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
-    etp_linear_kernel<T, P, BN><<<j.items < sms ? j.items : sms, kThreads, Lay::kBytes, s>>>(j);
+    etp_linear_kernel<T, P, BN, VEC, IMAGE><<<j.items < sms ? j.items : sms, Warps<P>::kThreads, Lay::kBytes, s>>>(j);
     return cudaGetLastError();
 }
 
-// Columns of a tile: the widest that still gives every SM a tile, or the narrowest.
-int tile_cols(int M, int N) {
-    const long long mt = (M + kRowsTile - 1) / kRowsTile;
+// VEC: the operands' rows move in 16-byte groups.
+template <typename T, Product P, int BN>
+cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
+    const bool z = !j.Z.rows.p || j.Z.vec;
+    if constexpr (P != Product::kGradW) {
+        if (image) {
+            using Lay = Layout<T, P, BN>;
+            const int rows = j.B.nrows, cols = j.B.ncols;
+            const int R = Lay::kBMn ? kStageK : BN, C = Lay::kBMn ? BN : kStageK;
+            const long long units = (long long)((rows + R - 1) / R) * ((cols + C - 1) / C) * (R * C / 8);
+            etp_linear_image_kernel<T, P, BN><<<(unsigned)((units + 255) / 256), 256, 0, s>>>(
+                static_cast<const T*>(j.B.rows.p), rows, cols, j.B.vec, image);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+            j.image = image;
+            return j.A.vec && z ? launch_kernel<T, P, BN, true, true>(j, s)
+                                : launch_kernel<T, P, BN, false, true>(j, s);
+        }
+    }
+    return j.A.vec && j.B.vec && z ? launch_kernel<T, P, BN, true, false>(j, s)
+                                   : launch_kernel<T, P, BN, false, false>(j, s);
+}
+
+// How the forward and grad_x products of M rows, k contracted and n output columns are
+// tiled: the widest tile that still gives every SM one, or the narrowest; and whether W
+// is converted ahead (an image), which pays once several row tiles share it.
+struct Tiling {
+    int bn;
+    bool image;
+    size_t image_bytes;
+};
+Tiling tiling(bool bf16, Product p, int M, int k, int n) {
+    const long long mt = ((long long)M + kRowsTile - 1) / kRowsTile;
     const int sms = sm_count();
-    if (N > 64 && mt * ((N + 127) / 128) >= sms) return 128;
-    if (N > 32 && mt * ((N + 63) / 64) >= sms) return 64;
-    return 32;
+    Tiling t;
+    t.bn = n > 64 && mt * ((n + 127) / 128) >= sms ? 128 : n > 32 && mt * ((n + 63) / 64) >= sms ? 64 : 32;
+    t.image = mt >= sms;
+    const size_t part = (size_t)(p == Product::kForward && t.bn < 64 ? 64 : t.bn) * kStageK * 2;
+    t.image_bytes =
+        t.image ? (size_t)((n + t.bn - 1) / t.bn) * ((k + kStageK - 1) / kStageK) * (bf16 ? 1 : 3) * part : 0;
+    return t;
 }
 
 template <typename T, Product P>
-cudaError_t launch(Job& j, int bn, int splits, cudaStream_t s) {
+cudaError_t launch(Job& j, int bn, int splits, unsigned char* image, cudaStream_t s) {
     j.ntn = (j.n + bn - 1) / bn;
     const long long tiles = (long long)((j.m + kRowsTile - 1) / kRowsTile) * j.ntn;
     if (tiles > 0x7fff0000LL) return cudaErrorInvalidValue;
@@ -647,9 +893,9 @@ cudaError_t launch(Job& j, int bn, int splits, cudaStream_t s) {
         j.items = j.tiles * splits;
     }
     switch (bn) {
-        case 128: return launch_bn<T, P, 128>(j, s);
-        case 64: return launch_bn<T, P, 64>(j, s);
-        default: return launch_bn<T, P, 32>(j, s);
+        case 128: return launch_bn<T, P, 128>(j, image, s);
+        case 64: return launch_bn<T, P, 64>(j, image, s);
+        default: return launch_bn<T, P, 32>(j, image, s);
     }
 }
 
@@ -684,11 +930,10 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t s) {
     j.map = a.map;
     j.out = a.out, j.z = a.z, j.residual = a.residual;
     j.bias = a.bias;
-    const bool n4 = a.N % 4 == 0;
-    j.vec_out = n4 && rows_aligned(a.out, elem, 4 * elem);
-    j.vec_z = n4 && rows_aligned(a.z, elem, 4 * elem);
-    j.vec_res = n4 && rows_aligned(a.residual, elem, 4 * elem);
-    return launch<T, Product::kForward>(j, tile_cols(j.m, j.n), 1, s);
+    j.vec_out = a.N % 2 == 0 && rows_aligned(a.out, elem, 2 * elem) && rows_aligned(a.z, elem, 2 * elem) &&
+                rows_aligned(a.residual, elem, 2 * elem) && (reinterpret_cast<uintptr_t>(a.bias) % (2 * elem)) == 0;
+    const Tiling t = tiling(elem == 2, Product::kForward, j.m, j.k, j.n);
+    return launch<T, Product::kForward>(j, t.bn, 1, t.image ? reinterpret_cast<unsigned char*>(a.ws) : nullptr, s);
 }
 
 template <typename T>
@@ -703,8 +948,10 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
         j.m = a.map.M, j.n = a.K, j.k = a.N;
         j.map = a.map;
         j.out = a.gx;
-        j.vec_out = a.K % 4 == 0 && rows_aligned(a.gx, elem, 4 * elem);
-        const cudaError_t e = launch<T, Product::kGradX>(j, tile_cols(j.m, j.n), 1, s);
+        j.vec_out = a.K % 2 == 0 && rows_aligned(a.gx, elem, 2 * elem);
+        const Tiling t = tiling(elem == 2, Product::kGradX, j.m, j.k, j.n);
+        const cudaError_t e = launch<T, Product::kGradX>(
+            j, t.bn, 1, t.image ? reinterpret_cast<unsigned char*>(a.ws) : nullptr, s);
         if (e != cudaSuccess) return e;
     }
     if (!a.gW && !a.gbias) return cudaSuccess;
@@ -713,10 +960,10 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
     const Ranges r = ranges(a.map.M, a.gW ? a.K : 1, a.N);
     const bool join = r.splits != 1;
     float* bias_part = a.gbias ? a.ws : nullptr;
-    float* part = a.ws + (size_t)r.splits * kLoadWarps * a.N;
+    float* part = a.ws + (size_t)r.splits * kBiasRows * a.N;
     if (r.splits > 0) {
         Job j;
-        j.A = operand(a.x, a.map, a.map.M, K, elem);
+        j.A = operand(a.gW ? a.x : a.g, a.map, a.map.M, K, elem);  // without grad_W: no columns, nothing read
         j.B = operand(a.g, a.map, a.map.M, a.N, elem);
         if (a.silu) j.Z = operand(a.z, a.map, a.map.M, a.N, elem);
         j.silu = a.silu;
@@ -725,16 +972,15 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
         j.gW = a.gW;
         j.part = join && a.gW ? part : nullptr;
         j.bias_part = bias_part;
-        j.vec_out = a.N % 4 == 0 && (j.part ? (reinterpret_cast<uintptr_t>(part) % 16) == 0
-                                            : (reinterpret_cast<uintptr_t>(a.gW) % (4 * elem)) == 0);
-        const cudaError_t e = launch<T, Product::kGradW>(j, r.bn, r.splits, s);
+        j.vec_out = a.N % 2 == 0 && (j.part || (reinterpret_cast<uintptr_t>(a.gW) % (2 * elem)) == 0);
+        const cudaError_t e = launch<T, Product::kGradW>(j, r.bn, r.splits, nullptr, s);
         if (e != cudaSuccess) return e;
     }
     const size_t count = a.gW && join ? (size_t)a.K * a.N : 0;
     const int blocks_w = (int)((count + 31) / 32), blocks_b = a.gbias ? (a.N + 31) / 32 : 0;
     if (blocks_w + blocks_b == 0) return cudaSuccess;
     etp_linear_join_kernel<T><<<blocks_w + blocks_b, 256, 0, s>>>(part, r.splits, count, static_cast<T*>(a.gW),
-                                                                  bias_part, r.splits * kLoadWarps, a.N,
+                                                                  bias_part, r.splits * kBiasRows, a.N,
                                                                   static_cast<T*>(a.gbias), blocks_w);
     return cudaGetLastError();
 }
@@ -746,11 +992,18 @@ cudaError_t linear_forward(bool bf16, const LinearArgs& a, cudaStream_t s) {
     return bf16 ? forward<__nv_bfloat16>(a, s) : forward<float>(a, s);
 }
 
-size_t linear_workspace_bytes(int M, int K, int N) {
-    const Ranges r = ranges(M, K, N), b = ranges(M, 1, N);  // grad_bias alone takes the second
-    const size_t sums = r.splits > 1 ? (size_t)r.splits * K * N : 0;
-    const int most = r.splits > b.splits ? r.splits : b.splits;
-    return (sums + (size_t)most * kLoadWarps * N) * sizeof(float);
+// The backward's two products use the workspace one after the other.
+size_t linear_workspace_bytes(bool bf16, int M, int K, int N, bool fwd, bool gx, bool gw, bool gb) {
+    size_t most = 0;
+    auto at_least = [&](size_t v) { most = v > most ? v : most; };
+    if (fwd) at_least(tiling(bf16, Product::kForward, M, K, N).image_bytes);
+    if (gx) at_least(tiling(bf16, Product::kGradX, M, N, K).image_bytes);
+    if (gw || gb) {
+        const Ranges r = ranges(M, gw ? K : 1, N);  // as backward() asks for them
+        at_least(((gw && r.splits > 1 ? (size_t)r.splits * K * N : 0) + (size_t)r.splits * kBiasRows * N) *
+                 sizeof(float));
+    }
+    return most;
 }
 
 cudaError_t linear_backward(bool bf16, const LinearArgs& a, cudaStream_t s) {

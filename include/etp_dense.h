@@ -55,34 +55,37 @@ typedef enum { ETP_ACT_NONE = 0, ETP_ACT_SILU = 1 } etp_activation;
 #define ETP_LINEAR_MAX_CHANNELS 65536
 #define ETP_NORM_MAX_CHANNELS 8192
 
+/* Bytes of device workspace that etp_linear_forward and etp_linear_backward need at
+ * most for these sizes (W rearranged for the tensor cores; partial sums of the weight
+ * gradients over ranges of rows). 0 is possible. Host only; it reads the current
+ * device's multiprocessor count. */
+ETP_API etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group, int K, int N,
+                                             size_t* bytes);
+
 /* Linear layer: z = x W + bias, out = act(z) + residual.
  * x: rows of K; W [K][N] row-major, contiguous; bias [N] or NULL; residual: rows of
  * N or NULL; z: rows of N, receives the pre-activation (rounded to the type; out is
  * computed from the unrounded value), or NULL; out: rows of N. act: ETP_ACT_NONE or
  * ETP_ACT_SILU (z / (1 + exp(-z))). residual may be out itself (same data and
- * strides): a residual stream updated in place.
+ * strides): a residual stream updated in place. workspace: etp_linear_workspace_size
+ * bytes, 16-byte aligned, owned by the caller (may be NULL when that is 0), free to
+ * reuse once the stream has passed the call.
  * Errors: ETP_ERR_INVALID_ARG for a negative size, K or N < 1 or above
- * ETP_LINEAR_MAX_CHANNELS, a NULL x, W or out, a negative stride, overlapping output
+ * ETP_LINEAR_MAX_CHANNELS, a NULL x, W or out, a stride that is negative or above 2^31 - 1, overlapping output
  * rows or a pointer misaligned for the type; ETP_ERR_UNSUPPORTED for an unknown
- * dtype or activation; ETP_ERR_TOO_LARGE when M is too large. */
+ * dtype or activation; ETP_ERR_TOO_LARGE when M is too large; ETP_ERR_WORKSPACE for a
+ * workspace that is too small. */
 ETP_API etp_status etp_linear_forward(etp_dtype dtype, int groups, int per_group, int K, int N, const etp_rows* x,
                                       const void* W, const void* bias, etp_activation act, const etp_rows* residual,
-                                      const etp_rows* z, const etp_rows* out, etp_stream_t stream);
-
-/* Bytes of device workspace etp_linear_backward needs (partial sums of the weight
- * gradients over row ranges). Host only; it reads the current device's
- * multiprocessor count. */
-ETP_API etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group, int K, int N,
-                                             size_t* bytes);
+                                      const etp_rows* z, const etp_rows* out, void* workspace,
+                                      size_t workspace_bytes, etp_stream_t stream);
 
 /* VJP of etp_linear_forward for the cotangent grad_out = dLoss/d(out), rows of N:
  *   dz = grad_out act'(z);  grad_x = dz W^T;  grad_W = x^T dz;  grad_bias = sum of dz over the rows
  * (the residual's gradient is grad_out itself). z: the forward's z, needed for
  * ETP_ACT_SILU, not read for ETP_ACT_NONE (NULL). grad_x (rows of K), grad_W [K][N],
  * grad_bias [N]: each may be NULL (skipped); x may be NULL when grad_W is, W when
- * grad_x is. workspace: etp_linear_workspace_size bytes, 16-byte aligned (may be
- * NULL when neither grad_W nor grad_bias is wanted). Errors as the forward's;
- * ETP_ERR_WORKSPACE for a workspace that is too small. */
+ * grad_x is. workspace and errors: as the forward's. */
 ETP_API etp_status etp_linear_backward(etp_dtype dtype, int groups, int per_group, int K, int N, const etp_rows* x,
                                        const void* W, etp_activation act, const etp_rows* z,
                                        const etp_rows* grad_out, const etp_rows* grad_x, void* grad_W,

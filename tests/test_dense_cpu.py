@@ -33,8 +33,9 @@ def test_exports_every_declared_symbol(lib):
 def test_linear_forward_refusals(lib):
     p = ctypes.c_void_p(PTR)
 
-    def call(dtype=0, groups=4, per=2, K=8, N=8, x=rows(), W=p, bias=p, act=1, res=rows(), z=rows(), out=rows()):
-        return lib.etp_linear_forward(dtype, groups, per, K, N, x, W, bias, act, res, z, out, None)
+    def call(dtype=0, groups=4, per=2, K=8, N=8, x=rows(), W=p, bias=p, act=1, res=rows(), z=rows(), out=rows(), ws=p,
+             n=1 << 40):
+        return lib.etp_linear_forward(dtype, groups, per, K, N, x, W, bias, act, res, z, out, ws, n, None)
 
     assert call(groups=-1) == call(per=-1) == call(K=0) == call(N=0) == BAD
     assert call(K=etp.LINEAR_MAX_CHANNELS + 1) == call(N=etp.LINEAR_MAX_CHANNELS + 1) == BAD
@@ -44,7 +45,7 @@ def test_linear_forward_refusals(lib):
     for name in ("x", "res", "z", "out"):  # misaligned for the type, negative or absurd strides
         assert call(**{name: rows(PTR + 2)}) == BAD
         assert call(**{name: rows(gs=-64)}) == call(**{name: rows(rs=-64)}) == BAD
-        assert call(**{name: rows(gs=1 << 41)}) == BAD
+        assert call(**{name: rows(gs=1 << 31)}) == BAD
     assert call(W=ctypes.c_void_p(PTR + 1)) == call(bias=ctypes.c_void_p(PTR + 2)) == BAD
     assert call(dtype=1, x=rows(PTR + 1)) == BAD
     for name in ("z", "out"):  # output rows that overlap
@@ -52,6 +53,9 @@ def test_linear_forward_refusals(lib):
         assert call(**{name: rows(gs=7, rs=64)}) == BAD
         assert call(**{name: rows(gs=12, rs=8)}) == BAD
         assert call(**{name: rows(gs=0, rs=8)}) == BAD
+    big = dict(groups=1 << 20, per=1)  # sizes that need a workspace
+    assert call(**big, ws=None) == call(**big, ws=ctypes.c_void_p(PTR + 8)) == BAD
+    assert call(**big, n=0) == WS
     assert call(groups=0, x=None, out=None, W=None) == OK  # nothing to do
     assert call(per=0, x=None, out=None, W=None) == OK
 
@@ -60,7 +64,7 @@ def test_linear_backward_refusals(lib):
     p = ctypes.c_void_p(PTR)
     size = ctypes.c_size_t()
     f = lib.etp_linear_workspace_size
-    assert f(0, 4, 2, 8, 8, ctypes.byref(size)) == OK
+    assert f(0, 4, 2, 8, 8, ctypes.byref(size)) == OK and size.value > 0
     assert f(0, 4, 2, 8, 8, None) == f(0, -1, 2, 8, 8, ctypes.byref(size)) == BAD
     assert f(0, 4, 2, 0, 8, ctypes.byref(size)) == f(0, 4, 2, 8, 0, ctypes.byref(size)) == BAD
     assert f(5, 4, 2, 8, 8, ctypes.byref(size)) == UNSUP
@@ -75,6 +79,8 @@ def test_linear_backward_refusals(lib):
     assert call(dtype=7) == call(act=9) == UNSUP
     assert call(gx=rows(rs=7)) == call(gx=rows(PTR + 2)) == BAD
     assert call(gW=ctypes.c_void_p(PTR + 2)) == call(gb=ctypes.c_void_p(PTR + 1)) == BAD
+    assert call(ws=None) == call(ws=ctypes.c_void_p(PTR + 4)) == BAD
+    assert call(n=0) == call(n=size.value - 1) == WS
     assert call(gx=None, gW=None, gb=None, x=None, W=None, z=None, g=None) == OK  # nothing wanted
     assert call(groups=1 << 20, per=1 << 11) == LARGE
 
