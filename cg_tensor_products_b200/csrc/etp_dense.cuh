@@ -103,7 +103,8 @@ __device__ __forceinline__ float sigmoid(float z) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
     return s;
 }
-__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
+// (a product of its own: never contracted with a sum, so a layer's result does not depend on what else it stores)
+__device__ __forceinline__ float silu(float z) { return __fmul_rn(z, sigmoid(z)); }
 __device__ __forceinline__ float silu_grad(float z) {
     const float s = sigmoid(z);
     return s * fmaf(z, 1.f - s, 1.f);

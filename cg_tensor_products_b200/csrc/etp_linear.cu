@@ -4,21 +4,27 @@
 //   backward  dz = g act'(z);  grad_x = dz W^T;  grad_W = x^T dz;  grad_bias = sum of dz over the rows
 //
 // Each of the three products is D[m][n] = sum_k A[m][k] B[k][n] in tiles of 128 x BN
-// outputs, 64 k per stage. One persistent CTA per SM:
-//   - loader warps read a stage of both operands from global memory into registers
-//     (the next one is in flight while the current one is converted), form dz where it
-//     is an operand, and store bfloat16 operands in the 128-byte-swizzled layouts of
-//     the tensor core: an operand whose contraction index is contiguous in memory
-//     K-major, one whose other index is contiguous MN-major, so nothing is transposed;
+// outputs, 32 or 64 k per stage. One persistent CTA per SM:
+//   - loader warps bring a stage's elements into shared memory by asynchronous copies, a
+//     few stages ahead, form dz where it is an operand, and hand over bfloat16 operands.
+//     A that has to be converted goes to tensor memory (lane = m), where the tensor core
+//     reads it without using shared memory's bandwidth, which bounds these kernels: a
+//     128 x 128 x 16 product reads 4 KB of B in its 64 cycles, with A in shared memory
+//     too all that there is. For grad_W the lane is a column of x, so its transposition
+//     is in the reading. B, and a bfloat16 A that is used as it is, lie in shared memory
+//     in the swizzled layouts of the tensor core: an operand whose contraction index is
+//     contiguous in memory K-major, one whose other index is contiguous MN-major;
+//   - W is converted ahead once where many row tiles share it, and its tiles arrive by
+//     bulk copies;
 //   - one warp issues the MMAs into a ring of accumulators in tensor memory;
 //   - epilogue warps add the accumulators up in registers and apply the epilogue.
 // Float32 operands are split by truncation into three bfloat16 parts x = x0 + x1 + x2
 // (8 bits each: exact), and a product is the sum of the six part products x0 w0, x0 w1,
 // x1 w0, x1 w1, x0 w2, x2 w0: what is left out is below 2^-22 of it. That is as many
 // MMAs as three TF32 products, at twice the mantissa of the smallest terms kept and in
-// three quarters of the shared memory, and both layouts are available to 16-bit types.
+// three quarters of the space, and both layouts are available to 16-bit types.
 // The tensor core truncates when it adds to its accumulator; so a float32 stage starts
-// a new accumulator, adds the small products first and the x0 w0 ones last (four
+// a new accumulator, adds the small products first and the x0 w0 ones last (up to four
 // truncated additions of full size), and stages are added up in registers, rounded to
 // nearest. bfloat16 operands are one part (dz is rounded to it: the tensor core reads
 // nothing wider beside bf16 weights without a second product); their accumulator holds
@@ -36,22 +42,22 @@ namespace {
 
 enum class Product { kForward, kGradX, kGradW };
 
-constexpr int kRowsTile = 128, kStageK = 64;
-// Warps: 8 of the epilogue, the loaders, one for the MMAs. Four loader warps leave 128
-// registers a thread (13 warps) for the epilogue's sums and the loads in flight; the
-// backward products, whose loaders have dz to compute and whose epilogue is plain, have
-// eight (17 warps, 96).
-constexpr int kEpiWarps = 8;
+constexpr int kRowsTile = 128;
+constexpr int kRangeK = 64;  // ranges of rows are whole multiples of it
+// Warps: the epilogue's (a quarter of the rows each, by a half or a quarter of the
+// columns), the loaders, one for the MMAs. The forward's epilogue has most to do and its
+// loaders least; the backward products have dz to compute in the loaders.
 template <Product P>
 struct Warps {
+    static constexpr int kEpi = P == Product::kForward ? 16 : 8;
     static constexpr int kLoad = P == Product::kForward ? 4 : 8;
-    static constexpr int kLoaders = 32 * kLoad;
-    static constexpr int kMma = kEpiWarps + kLoad;
+    static constexpr int kMma = kEpi + kLoad;
     static constexpr int kThreads = 32 * (kMma + 1);
+    static constexpr int kLoaders = 32 * kLoad;
 };
 constexpr int kBiasRows = Warps<Product::kGradW>::kLoad;  // partial sums of dz per range: one per loader warp
 constexpr int kWaitLimit = 1 << 22;
-constexpr int kRing = 4;               // accumulators in tensor memory
+constexpr int kRing = 2;  // accumulators in tensor memory
 constexpr uint32_t kSmemMost = 232448;
 
 __device__ int g_fault;
@@ -63,25 +69,88 @@ struct Int {
 
 template <typename T>
 constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+// k of a stage. grad_W's float32 stages are half as long: they hold three operands.
+template <typename T, Product P>
+constexpr int kStageK = sizeof(T) == 4 && P == Product::kGradW ? 32 : 64;
 // Stages that one accumulator holds.
 template <typename T>
 constexpr int kChunk = sizeof(T) == 4 ? 1 : 16;
 
-// Shared memory of one instance: slots of A and B parts, barriers.
-template <typename T, Product P, int BN>
+// Swizzled bf16 operand layouts in shared memory: rows of 128 bytes, the 16-byte chunk
+// index XORed with the row mod 8. MN-major: rows are k, 64 m (n) across; groups of 8 k
+// 1024 bytes apart (SBO), panels of 64 m (n) K * 128 bytes apart (LBO). K-major: rows are
+// m (n), 64 k across, groups of 8 rows 1024 bytes apart.
+template <bool MN, int K>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    static_assert(MN || K == 64, "K-major rows of 128 bytes");
+    constexpr uint64_t lbo = MN ? (K * 128 >> 4) : 1, sbo = 1024 >> 4;
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (lbo << 16) | (sbo << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Byte offset of the 16-byte chunk c of source row r in an operand part.
+template <int K>
+__host__ __device__ constexpr uint32_t chunk_offset(int r, int c) {
+    return (uint32_t)(c >> 3) * (K * 128) + (uint32_t)(r >> 3) * 1024 + (uint32_t)(r & 7) * 128 +
+           (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// A loader's share of an operand tile of ROWS source rows by COLS columns: units of 8
+// columns, unit u = t + THREADS i at row u / (COLS / 8).
+template <int ROWS, int COLS, int K, int THREADS>
+struct Share {
+    static constexpr int kPerRow = COLS / 8;
+    static constexpr int kIters = (ROWS * kPerRow + THREADS - 1) / THREADS;
+    static constexpr bool kEven = ROWS * kPerRow % THREADS == 0;  // or the last threads have none
+    static __device__ __forceinline__ int row(int t, int i) { return (t + THREADS * i) / kPerRow; }
+    static __device__ __forceinline__ int col(int t) { return t % kPerRow; }
+    static __device__ __forceinline__ bool has(int t, int i) { return kEven || t + THREADS * i < ROWS * kPerRow; }
+    static __device__ __forceinline__ uint32_t offset(int t, int i) { return chunk_offset<K>(row(t, i), col(t)); }
+};
+
+// The tile shapes and memory of one instance. VEC: the operands' rows move in 16-byte
+// groups. IMAGE: B arrives as ready tiles.
+template <typename T, Product P, int BN, bool VEC, bool IMAGE>
 struct Layout {
-    static constexpr bool kAMn = P == Product::kGradW;   // A is MN-major (contraction over rows)
-    static constexpr bool kBMn = P != Product::kGradX;   // B likewise
-    static constexpr uint32_t kAPart = kRowsTile * kStageK * 2;
-    static constexpr uint32_t kBPart = kBMn && BN < 64 ? 64u * kStageK * 2 : (uint32_t)BN * kStageK * 2;
-    static constexpr uint32_t kSlot = kParts<T> * (kAPart + kBPart);
+    using W = Warps<P>;
+    static constexpr int kK = kStageK<T, P>;
+    static constexpr bool kAMn = P == Product::kGradW;  // A is MN-major (contraction over rows)
+    static constexpr bool kBMn = P != Product::kGradX;  // B likewise
+    static constexpr bool kDzA = P == Product::kGradX, kDzB = P == Product::kGradW;
+    static constexpr bool kTmemA = sizeof(T) == 4 || kDzA;  // A is converted
+    static constexpr bool kConvB = !IMAGE && (sizeof(T) == 4 || kDzB);  // B is converted here
+    static constexpr bool kCopyB = !IMAGE && !kConvB;                   // or used as it is
+    using ShareA = Share<kAMn ? kK : kRowsTile, kAMn ? kRowsTile : kK, kK, W::kLoaders>;
+    using ShareB = Share<kBMn ? kK : BN, kBMn ? BN : kK, kK, W::kLoaders>;
+    // A slot: B's parts and an A that is used as it is; a converted A's parts have columns in tensor memory
+    static constexpr uint32_t kAPart = kTmemA ? 0 : kRowsTile * kK * 2;
+    static constexpr uint32_t kBPart = (kBMn && BN < 64 ? 64u : (uint32_t)BN) * kK * 2;
+    static constexpr uint32_t kSlot = kParts<T> * kBPart + kAPart;
+    static constexpr uint32_t kACols = kTmemA ? kParts<T> * kK / 2 : 0;
+    // Elements on their way, per stage: of A, of the pre-activation beside dz, of B
+    static constexpr uint32_t kRawA = kTmemA ? kRowsTile * kK * sizeof(T) : 0;
+    static constexpr uint32_t kRawB = kConvB ? ShareB::kIters * W::kLoaders * 8 * sizeof(T) : 0;
+    static constexpr uint32_t kRawZ = kDzA ? kRawA : kDzB ? kRawB : 0;
+    static constexpr uint32_t kRaw = kRawA + kRawZ + kRawB;
     static constexpr uint32_t kTail = 256;  // barriers
-    static constexpr int kFit = (int)((kSmemMost - kTail) / kSlot);
-    static constexpr int kSlots = kFit < 6 ? kFit : 6;
-    static constexpr uint32_t kOffBars = kSlots * kSlot;
+    static constexpr int kWant = 3;         // slots, where there is room
+    static constexpr int kTmemSlots = kACols ? (int)((512 - kRing * BN) / kACols) : 8;
+    static constexpr int kFew = kTmemSlots < 2 + (kSlot <= 32768) ? kTmemSlots : 2 + (kSlot <= 32768);
+    // Stages in flight. Copies straight into a slot share their groups, and the slot's hand-over lags behind by
+    // as many; without other elements on their way they use the slots themselves.
+    static constexpr int kMost = !kTmemA || kCopyB ? kFew - 1 : 3;
+    static constexpr int kRoom = kRaw ? (int)((kSmemMost - kTail - kFew * kSlot) / kRaw) : 1;
+    static constexpr int kDepth = kRoom < kMost ? kRoom : kMost;
+    static constexpr int kFit = (int)((kSmemMost - kTail - kDepth * kRaw) / kSlot);
+    static constexpr int kCap = kTmemSlots < (kRaw ? kWant + 1 : 6) ? kTmemSlots : (kRaw ? kWant + 1 : 6);
+    static constexpr int kSlots = kFit < kCap ? kFit : kCap;
+    static constexpr int kLag = kTmemA && !kCopyB ? 0 : kRaw ? kDepth : kSlots - 1;
+    static constexpr uint32_t kOffRaw = kSlots * kSlot;
+    static constexpr uint32_t kOffBars = kOffRaw + kDepth * kRaw;
     static constexpr uint32_t kBytes = kOffBars + kTail;
-    static constexpr uint32_t kTmemCols = kRing * BN;
-    static_assert(kSlots >= 2 && kBytes <= kSmemMost && kTmemCols <= 512, "linear layer shared memory");
+    static constexpr uint32_t kTmemCols = kRing * BN + kSlots * kACols <= 128   ? 128
+                                          : kRing * BN + kSlots * kACols <= 256 ? 256
+                                                                                : 512;
+    static_assert(kSlots >= 2 && kDepth >= 1 && kLag < kSlots && kBytes <= kSmemMost, "linear layer memory");
+    static_assert(kRing * BN + kSlots * kACols <= 512, "linear layer tensor memory");
 };
 
 // An operand as the loaders see it: source rows of ncols contiguous elements.
@@ -96,8 +165,10 @@ struct Job {
     Operand A, B, Z;  // Z: the pre-activation beside dz
     int silu = 0;
     int m = 0, n = 0, k = 0;  // extents of the product
-    int ntn = 1, items = 1;   // tiles along n; work items
-    int tiles = 1, range = 0; // grad_W: tiles of the output, rows per range
+    FastDiv ntn;              // tiles along n
+    int items = 1;            // work items
+    FastDiv tiles;            // grad_W: tiles of the output
+    int range = 0;            // and rows per range
     RowMap map;               // rows of the output operands
     Rows out, z, residual;
     const void* bias = nullptr;
@@ -107,37 +178,13 @@ struct Job {
     const unsigned char* image = nullptr;  // B as tiles of operand parts, or null
 };
 
-// Loads under a predicate, zeros where it is false. The predicate is inside the
-// instruction: a branch around a load would make the warp wait for it at the join.
-__device__ __forceinline__ uint4 ldg16(const void* p, bool on) {
-    uint4 v;
-    asm volatile(
-        "{\n .reg .pred pp;\n setp.ne.b32 pp, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
-        " mov.u32 %3, 0;\n @pp ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((int)on));
-    return v;
-}
-__device__ __forceinline__ uint32_t ldg_elem(const float* p, bool on) {
-    uint32_t v;
-    asm volatile("{\n .reg .pred pp;\n setp.ne.b32 pp, %2, 0;\n mov.u32 %0, 0;\n @pp ld.global.nc.u32 %0, [%1];\n}"
-                 : "=&r"(v)
-                 : "l"(p), "r"((int)on));
-    return v;
-}
-__device__ __forceinline__ uint32_t ldg_elem(const __nv_bfloat16* p, bool on) {
-    uint32_t v;
-    asm volatile(
-        "{\n .reg .pred pp;\n .reg .u16 h;\n setp.ne.b32 pp, %2, 0;\n mov.u16 h, 0;\n @pp ld.global.nc.u16 h, [%1];\n"
-        " cvt.u32.u16 %0, h;\n}"
-        : "=&r"(v)
-        : "l"(p), "r"((int)on));
-    return v;
-}
-
-// 16 bytes of global memory into shared memory asynchronously, zeros where `on` is false.
+// Asynchronous copies into shared memory, zeros where `on` is false.
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(on ? 4 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -145,50 +192,61 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// 16 bytes of a row of which `left` elements remain: one copy, or element by element where
+// rows are not aligned (float32 still asynchronously; bfloat16 elements are narrower than
+// the narrowest asynchronous copy and pass through registers).
+template <typename T, bool VEC>
+__device__ __forceinline__ void copy_chunk(unsigned char* dst, const T* p, int left) {
+    if constexpr (VEC) {
+        copy16(dst, p, left > 0);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) copy4(dst + 4 * j, p + j, left > j);
+    } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            asm volatile(
+                "{\n .reg .pred pp;\n .reg .u16 h;\n setp.ne.b32 pp, %2, 0;\n mov.u16 h, 0;\n"
+                " @pp ld.global.nc.u16 h, [%1];\n cvt.u32.u16 %0, h;\n}"
+                : "=&r"(v[j])
+                : "l"(p + j), "r"((int)(left > j)));
+        *reinterpret_cast<uint4*>(dst) =
+            make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
 
-// Eight consecutive elements of a row as they lie in memory, zeros past the `left` that remain.
+// Copies of one operand tile: `n` chunks a lane, chunk i (DR i) rows below the lane's
+// first and in the same columns. On one row stride that is a fixed distance in memory.
+template <typename T, bool VEC, int N, int DR, typename Dst>
+__device__ __forceinline__ void copy_column(const Operand& o, int r0, int rlim, int c, Dst&& dst) {
+    const int left = o.ncols - c;
+    if (o.map.per.d == 1) {
+        const T* p = static_cast<const T*>(o.rows.p) + (unsigned long long)(unsigned)r0 * o.rows.gs + c;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_chunk<T, VEC>(dst(i), p + (unsigned long long)(DR * i) * o.rows.gs, r0 + DR * i < rlim ? left : 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = r0 + DR * i;
+            copy_chunk<T, VEC>(dst(i), static_cast<const T*>(o.rows.p) + o.rows.offset(o.map, r) + c,
+                               r < rlim ? left : 0);
+        }
+    }
+}
+
+// 16 bytes of shared memory as floats.
 template <typename T>
-struct Unit;
-template <>
-struct Unit<float> {
-    uint4 a, b;
-    template <bool VEC>
-    __device__ __forceinline__ void load(const float* p, int left) {
-        if constexpr (VEC) {
-            a = ldg16(p, left >= 4);
-            b = ldg16(p + 4, left >= 8);
-        } else {
-            a = make_uint4(ldg_elem(p, left > 0), ldg_elem(p + 1, left > 1), ldg_elem(p + 2, left > 2),
-                           ldg_elem(p + 3, left > 3));
-            b = make_uint4(ldg_elem(p + 4, left > 4), ldg_elem(p + 5, left > 5), ldg_elem(p + 6, left > 6),
-                           ldg_elem(p + 7, left > 7));
-        }
+__device__ __forceinline__ void read16(const unsigned char* p, float* v) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    if constexpr (sizeof(T) == 4) {
+        v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+    } else {
+        v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+        v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z);
-        v[3] = __uint_as_float(a.w), v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y);
-        v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-    }
-};
-template <>
-struct Unit<__nv_bfloat16> {
-    uint4 a;
-    template <bool VEC>
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, int left) {
-        if constexpr (VEC) {
-            a = ldg16(p, left >= 8);
-        } else {
-            a = make_uint4(ldg_elem(p, left > 0) | ldg_elem(p + 1, left > 1) << 16,
-                           ldg_elem(p + 2, left > 2) | ldg_elem(p + 3, left > 3) << 16,
-                           ldg_elem(p + 4, left > 4) | ldg_elem(p + 5, left > 5) << 16,
-                           ldg_elem(p + 6, left > 6) | ldg_elem(p + 7, left > 7) << 16);
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
-        v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
-    }
-};
+}
 
 // High halves of two floats as a bf16 pair (truncation).
 __device__ __forceinline__ uint32_t high_pair(float a, float b) {
@@ -196,40 +254,38 @@ __device__ __forceinline__ uint32_t high_pair(float a, float b) {
 }
 __device__ __forceinline__ float high_part(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
-// Eight floats into the operand parts at `dst` (part stride bytes): three truncated
+// The parts of N floats, part after part, as bf16 pairs: emit(p, pairs). Three truncated
 // parts of a float32 operand, one rounded part of a bf16 one.
-template <typename T>
-__device__ __forceinline__ void store_parts(unsigned char* dst, uint32_t part, float (&v)[8]) {
+template <typename T, int N, typename Emit>
+__device__ __forceinline__ void split_parts(float (&v)[N], Emit&& emit) {
+    uint32_t w[N / 2];
     if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                    pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+#pragma unroll
+        for (int j = 0; j < N; j += 2) w[j / 2] = pack_bf16(v[j], v[j + 1]);
+        emit(0, w);
     } else {
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-            *reinterpret_cast<uint4*>(dst + p * part) = make_uint4(high_pair(v[0], v[1]), high_pair(v[2], v[3]),
-                                                                   high_pair(v[4], v[5]), high_pair(v[6], v[7]));
+#pragma unroll
+            for (int j = 0; j < N; j += 2) w[j / 2] = high_pair(v[j], v[j + 1]);
+            emit(p, w);
             if (p < 2)
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {  // packed: v - high_part(v)
-                    const float2 r = __fadd2_rn(make_float2(v[j], v[j + 1]),
-                                                make_float2(-high_part(v[j]), -high_part(v[j + 1])));
+                for (int j = 0; j < N; j += 2) {  // packed: v - high_part(v), exact
+                    const float2 r = __ffma2_rn(make_float2(high_part(v[j]), high_part(v[j + 1])),
+                                                make_float2(-1.f, -1.f), make_float2(v[j], v[j + 1]));
                     v[j] = r.x, v[j + 1] = r.y;
                 }
         }
     }
 }
-
-// Descriptors of the 128-byte-swizzled bf16 layouts. Atoms of 8 rows x 128 bytes, the
-// 16-byte chunk index XORed with the row. K-major: rows are m (n), 64 k across, SBO =
-// 1024 bytes between groups of 8 rows. MN-major: rows are k, 64 m (n) across; SBO =
-// 1024 between groups of 8 k, LBO between panels of 64 m (n).
-constexpr uint32_t kPanel = kStageK * 128;  // MN-major panel: 64 k rows of 128 bytes
-template <bool MN>
-__device__ __forceinline__ uint64_t desc128(uint32_t saddr) {
-    const uint64_t lbo = MN ? (kPanel >> 4) : 1;
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (lbo << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-           ((uint64_t)2 << 61);
+template <typename T>
+__device__ __forceinline__ void store_parts(unsigned char* dst, uint32_t part, float (&v)[8]) {
+    split_parts<T, 8>(v, [&](int p, const uint32_t(&w)[4]) {
+        *reinterpret_cast<uint4*>(dst + p * part) = make_uint4(w[0], w[1], w[2], w[3]);
+    });
 }
+
 // D f32, A and B bf16, shape 128 x n.
 template <bool AMN, bool BMN>
 constexpr uint32_t idesc_bf16(int n) {
@@ -243,14 +299,25 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t da, uint64_t db, u
         "l"(da), "l"(db), "r"(idesc), "r"(acc)
         : "memory");
 }
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred pp;\n setp.ne.b32 pp, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pp;\n}" ::"r"(d),
+        "r"(a), "l"(db), "r"(idesc), "r"(acc)
+        : "memory");
+}
 
-// Two elements of a row, zeros past the `left` that remain. V: both at once (they are
-// aligned and `left` is not 1). The statements are volatile, so that they stay in order:
-// a residual that is the output is read before it is written, and one row at a time.
-template <bool V>
+// How an epilogue moves two elements of a row: whole pairs inside a tile that has all its
+// rows (at one stride) and columns, whole pairs under a predicate (an even number of columns), or single
+// elements. Zeros are read past the `left` that remain. The predicated statements are
+// volatile, so that they stay in order: a residual that is the output is read before it
+// is written.
+enum class Pairs { kFull, kEven, kAny };
+template <Pairs V>
 __device__ __forceinline__ float2 load2(const float* p, int left) {
     float a, b;
-    if constexpr (V)
+    if constexpr (V == Pairs::kFull) return *reinterpret_cast<const float2*>(p);
+    if constexpr (V == Pairs::kEven)
         asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %3, 0;\n mov.f32 %0, 0f00000000;\n mov.f32 %1, 0f00000000;\n"
             " @pp ld.global.v2.f32 {%0, %1}, [%2];\n}"
             : "=&f"(a), "=&f"(b)
@@ -262,10 +329,12 @@ __device__ __forceinline__ float2 load2(const float* p, int left) {
             : "l"(p), "r"(left));
     return make_float2(a, b);
 }
-template <bool V>
+template <Pairs V>
 __device__ __forceinline__ float2 load2(const __nv_bfloat16* p, int left) {
     uint32_t a;
-    if constexpr (V)
+    if constexpr (V == Pairs::kFull)
+        a = *reinterpret_cast<const uint32_t*>(p);
+    else if constexpr (V == Pairs::kEven)
         asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %2, 0;\n mov.u32 %0, 0;\n @pp ld.global.u32 %0, [%1];\n}"
             : "=&r"(a)
             : "l"(p), "r"(left));
@@ -277,9 +346,11 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p, int left) {
             : "l"(p), "r"(left));
     return make_float2(bf16_lo(a), bf16_hi(a));
 }
-template <bool V>
+template <Pairs V>
 __device__ __forceinline__ void store2(float* p, float2 v, int left) {
-    if constexpr (V)
+    if constexpr (V == Pairs::kFull)
+        *reinterpret_cast<float2*>(p) = v;
+    else if constexpr (V == Pairs::kEven)
         asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %3, 0;\n @pp st.global.v2.f32 [%0], {%1, %2};\n}" ::"l"(p),
                      "f"(v.x), "f"(v.y), "r"(left));
     else
@@ -287,10 +358,12 @@ __device__ __forceinline__ void store2(float* p, float2 v, int left) {
                      " @p0 st.global.f32 [%0], %1;\n @p1 st.global.f32 [%0+4], %2;\n}" ::"l"(p),
                      "f"(v.x), "f"(v.y), "r"(left));
 }
-template <bool V>
+template <Pairs V>
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v, int left) {
     const uint32_t a = pack_bf16(v.x, v.y);
-    if constexpr (V)
+    if constexpr (V == Pairs::kFull)
+        *reinterpret_cast<uint32_t*>(p) = a;
+    else if constexpr (V == Pairs::kEven)
         asm volatile("{\n .reg .pred pp;\n setp.gt.s32 pp, %2, 0;\n @pp st.global.u32 [%0], %1;\n}" ::"l"(p), "r"(a),
                      "r"(left));
     else
@@ -303,139 +376,131 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v, int left) {
 struct Item {
     int m0, n0, k0, k1, split, stages;
 };
-template <Product P>
+template <typename T, Product P>
 __device__ __forceinline__ Item item_of(const Job& j, int i, int bn) {
     Item it;
     int tile = i;
     it.split = 0, it.k0 = 0, it.k1 = j.k;
     if (P == Product::kGradW) {
-        it.split = i / j.tiles;
-        tile = i - it.split * j.tiles;
+        it.split = (int)j.tiles.quot(i);
+        tile = i - it.split * j.tiles.d;
         it.k0 = it.split * j.range;
         it.k1 = min(j.k, it.k0 + j.range);
     }
-    const int mt = tile / j.ntn;
+    const int mt = (int)j.ntn.quot(tile);
     it.m0 = mt * kRowsTile;
-    it.n0 = (tile - mt * j.ntn) * bn;
-    it.stages = (it.k1 - it.k0 + kStageK - 1) / kStageK;
+    it.n0 = (tile - mt * j.ntn.d) * bn;
+    it.stages = (it.k1 - it.k0 + kStageK<T, P> - 1) / kStageK<T, P>;
     return it;
 }
 
-// The epilogue of a tile on one warp's 32 rows x BN / 2 columns, in the accumulator's
+// The epilogue of a tile on one warp's 32 rows x COLS columns, in the accumulator's
 // fragment layout: a lane holds 4 rows, of each 2 neighbouring columns in every 8. The 4
 // lanes of a row make whole 32-byte sectors of float32, so loads and stores go straight
-// between registers and memory, and a lane has 4 row addresses, not one per element.
-// V: every operand of the epilogue moves 2 elements at a time.
-template <typename T, Product P, int BN, bool V>
-__device__ __forceinline__ void finish(const Job& job, const Item& it, float (&acc)[2][BN / 4], int quad, int half,
+// between registers and memory.
+template <Pairs V>
+__device__ __forceinline__ unsigned long long row_offset(const Job& job, const Rows& r, int m) {
+    return V == Pairs::kFull ? (unsigned long long)(unsigned)m * r.gs : r.offset(job.map, m);
+}
+template <typename T, Product P, int COLS, Pairs V>
+__device__ __forceinline__ void finish(const Job& job, const Item& it, float (&acc)[2][COLS / 2], int quad, int part,
                                        int lane) {
-    constexpr int kGroups = BN / 16;  // groups of 8 columns
-    const int n0 = it.n0 + half * (BN / 2) + 2 * (lane & 3);
+    constexpr int kGroups = COLS / 8 < 4 ? COLS / 8 : 4;  // groups of 8 columns at a time
     const bool has_res = P == Product::kForward && job.residual.p != nullptr;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int m = it.m0 + quad * 32 + 8 * r + (lane >> 2);
-        const int left = m < job.m ? job.n - n0 : 0;
-        float2 v[kGroups];
-#pragma unroll
-        for (int c = 0; c < kGroups; ++c)
-            v[c] = make_float2(acc[r >> 1][4 * c + 2 * (r & 1)], acc[r >> 1][4 * c + 2 * (r & 1) + 1]);
+    for (int g = 0; g < COLS / 8; g += kGroups) {
+        const int n = it.n0 + part * COLS + 8 * g + 2 * (lane & 3);
+        float2 bias[kGroups];
         if constexpr (P == Product::kForward) {
-            float2 res[kGroups];
-            if (has_res) {
-                const T* p = static_cast<const T*>(job.residual.p) + job.residual.offset(job.map, m) + n0;
 #pragma unroll
-                for (int c = 0; c < kGroups; ++c) res[c] = load2<V>(p + 8 * c, left - 8 * c);
+            for (int c = 0; c < kGroups; ++c) {
+                bias[c] = make_float2(0.f, 0.f);
+                if (job.bias) bias[c] = load2<V>(static_cast<const T*>(job.bias) + n + 8 * c, job.n - n - 8 * c);
             }
-            if (job.bias) {
-                const T* p = static_cast<const T*>(job.bias) + n0;
+        }
 #pragma unroll
-                for (int c = 0; c < kGroups; ++c) {
-                    const float2 b = load2<V>(p + 8 * c, job.n - n0 - 8 * c);
-                    v[c].x += b.x, v[c].y += b.y;
+        for (int r0 = 0; r0 < 4; r0 += 2) {  // two rows at a time
+            float2 res[2][kGroups];
+            int left[2];
+            unsigned long long off[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int m = it.m0 + quad * 32 + 8 * (r0 + q) + (lane >> 2);
+                left[q] = V == Pairs::kFull || m < job.m ? job.n - n : 0;
+                off[q] = n + (P == Product::kGradW ? (unsigned long long)m * job.n : row_offset<V>(job, job.out, m));
+                if (has_res) {
+                    const T* p = static_cast<const T*>(job.residual.p) + row_offset<V>(job, job.residual, m) + n;
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) res[q][c] = load2<V>(p + 8 * c, left[q] - 8 * c);
                 }
             }
-            if (job.z.p) {
-                T* p = static_cast<T*>(job.z.p) + job.z.offset(job.map, m) + n0;
 #pragma unroll
-                for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
+            for (int q = 0; q < 2; ++q) {
+                const int r = r0 + q;
+                float2 v[kGroups];
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c)
+                    v[c] = make_float2(acc[r >> 1][4 * (g + c) + 2 * (r & 1)], acc[r >> 1][4 * (g + c) + 2 * (r & 1) + 1]);
+                if constexpr (P == Product::kForward) {
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) v[c].x += bias[c].x, v[c].y += bias[c].y;
+                    if (job.z.p) {
+                        const int m = it.m0 + quad * 32 + 8 * r + (lane >> 2);
+                        T* p = static_cast<T*>(job.z.p) + row_offset<V>(job, job.z, m) + n;
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left[q] - 8 * c);
+                    }
+                    if (job.silu)
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c) v[c].x = silu(v[c].x), v[c].y = silu(v[c].y);
+                    if (has_res)
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c) v[c].x += res[q][c].x, v[c].y += res[q][c].y;
+                }
+                if (P == Product::kGradW && job.part) {
+                    float* p = job.part + (size_t)it.split * job.m * job.n + off[q];
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left[q] - 8 * c);
+                } else {
+                    T* p = (P == Product::kGradW ? static_cast<T*>(job.gW) : static_cast<T*>(job.out.p)) + off[q];
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left[q] - 8 * c);
+                }
             }
-            if (job.silu)
-#pragma unroll
-                for (int c = 0; c < kGroups; ++c) v[c].x = silu(v[c].x), v[c].y = silu(v[c].y);
-            if (has_res)
-#pragma unroll
-                for (int c = 0; c < kGroups; ++c) v[c].x += res[c].x, v[c].y += res[c].y;
-        }
-        if (P == Product::kGradW && job.part) {
-            float* p = job.part + ((size_t)it.split * job.m + m) * job.n + n0;
-#pragma unroll
-            for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
-        } else {
-            T* p = P == Product::kGradW ? static_cast<T*>(job.gW) + (size_t)m * job.n + n0
-                                        : static_cast<T*>(job.out.p) + job.out.offset(job.map, m) + n0;
-#pragma unroll
-            for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
         }
     }
 }
 
-// A loader's share of an operand tile of ROWS source rows by COLS columns: units of 8
-// columns, unit u = t + 256 i at row u / (COLS / 8).
-template <int ROWS, int COLS, int kLoaders>
-struct Share {
-    static constexpr int kPerRow = COLS / 8;
-    static constexpr int kIters = ROWS * kPerRow / kLoaders;
-    static_assert(kIters >= 1 && ROWS * kPerRow % kLoaders == 0, "loader share");
-    static __device__ __forceinline__ int row(int t, int i) { return (t + kLoaders * i) / kPerRow; }
-    static __device__ __forceinline__ int col(int t) { return t % kPerRow; }
-    static __device__ __forceinline__ uint32_t offset(int t, int i) {
-        const int r = row(t, i), c = col(t);
-        return (uint32_t)(c >> 3) * kPanel + (uint32_t)(r >> 3) * 1024 + (uint32_t)(r & 7) * 128 +
-               (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-    }
-};
-
-// IMAGE: B arrives as ready tiles (etp_linear_image_kernel) by bulk copies.
 template <typename T, Product P, int BN, bool VEC, bool IMAGE>
 __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const __grid_constant__ Job job) {
-    using Lay = Layout<T, P, BN>;
-    constexpr int NP = kParts<T>;
-    constexpr int kLoadWarps = Warps<P>::kLoad, kLoaders = Warps<P>::kLoaders, kMmaWarp = Warps<P>::kMma;
-    constexpr bool kDzA = P == Product::kGradX, kDzB = P == Product::kGradW;
-    // bfloat16 operands that need no arithmetic are copied straight to shared memory
-    constexpr bool kCopyA = sizeof(T) == 2 && VEC && !kDzA, kCopyB = sizeof(T) == 2 && VEC && !kDzB && !IMAGE;
-    constexpr bool kCopies = kCopyA || kCopyB;
-    constexpr bool kRegA = !kCopyA, kRegB = !kCopyB && !IMAGE;
-    constexpr int kDepth = Lay::kSlots - 1;  // stages of copies in flight
-    // parts of a stage that a loader holds in flight in turn, as registers allow
-    constexpr int kHalves = IMAGE || sizeof(T) == 2 ? (P == Product::kForward ? 1 : 2) : P == Product::kGradX ? 4 : 2;
-    using ShareA = Share<Lay::kAMn ? kStageK : kRowsTile, Lay::kAMn ? kRowsTile : kStageK, kLoaders>;
-    using ShareB = Share<Lay::kBMn ? kStageK : BN, Lay::kBMn ? BN : kStageK, kLoaders>;
-    constexpr int IA = ShareA::kIters, IB = ShareB::kIters;
-    constexpr int HA = (IA + kHalves - 1) / kHalves, HB = (IB + kHalves - 1) / kHalves;  // units of a part
+    using Lay = Layout<T, P, BN, VEC, IMAGE>;
+    using W = Warps<P>;
+    using ShareA = typename Lay::ShareA;
+    using ShareB = typename Lay::ShareB;
+    constexpr int NP = kParts<T>, K = Lay::kK, kSlots = Lay::kSlots;
+    constexpr bool kDzA = Lay::kDzA, kDzB = Lay::kDzB;
 
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBars);  // a slot's operands are written
-    uint64_t* bfull = full + Lay::kSlots;                                 // its image tile has arrived
-    uint64_t* empty = bfull + Lay::kSlots;                                // its MMAs are done
-    uint64_t* tfull = empty + Lay::kSlots;                                // an accumulator is complete
+    uint64_t* bfull = full + kSlots;                                      // its image tile has arrived
+    uint64_t* empty = bfull + kSlots;                                     // its MMAs are done
+    uint64_t* tfull = empty + kSlots;                                     // an accumulator is complete
     uint64_t* tempty = tfull + kRing;                                     // and has been read
     uint64_t* drain = tempty + kRing;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
-    if (warp == kMmaWarp) tc::tmem_alloc(tmem_slot, Lay::kTmemCols);
+    if (warp == W::kMma) tc::tmem_alloc(tmem_slot, Lay::kTmemCols);
     if (t == 0) {
-        for (int i = 0; i < Lay::kSlots; ++i) {
-            tc::mbar_init(&full[i], kLoadWarps);
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(&full[i], W::kLoad);
             tc::mbar_init(&bfull[i], 1);
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
             tc::mbar_init(&tfull[i], 1);
-            tc::mbar_init(&tempty[i], kEpiWarps);
+            tc::mbar_init(&tempty[i], W::kEpi);
         }
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -445,6 +510,7 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem_a = tmem + kRing * BN;  // converted A: per slot, part after part
     // A bounded wait; false: leave the loops. wait(): the same answer for the whole warp.
     auto wait1 = [&](uint64_t* bar, unsigned parity) {
         const bool ok = !*abort_flag && tc::mbar_wait(bar, parity, kWaitLimit);
@@ -452,180 +518,206 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
         return ok;
     };
     auto wait = [&](uint64_t* bar, unsigned parity) { return __all_sync(0xffffffffu, wait1(bar, parity)) != 0; };
-    int images = 0;  // (loader thread 0) image tiles asked for
+    int images = 0;  // (first loader thread) image tiles asked for
 
-    if (warp >= kEpiWarps && warp < kMmaWarp) {  // loaders
-        const int lt = t - 32 * kEpiWarps;
-        Unit<T> ra[kRegA ? HA : 1], rb[kRegB ? HB : 1], rz[kDzA ? HA : kDzB ? HB : 1];
-        // Two cursors: the stage that is stored now, and the one that is fetched into registers.
+    if (warp >= W::kEpi && warp < W::kMma) {  // loaders
+        const int lt = t - 32 * W::kEpi, lw = lt >> 5;
+        // Two cursors: the stage that is handed over now, and the one that is fetched, kDepth ahead.
         struct Cursor {
             int i, ks;
             Item it;
-        } now{(int)blockIdx.x, 0, item_of<P>(job, blockIdx.x, BN)}, next = now;
-        auto advance = [&](Cursor& c) {  // true: another item
-            if (++c.ks < c.it.stages) return false;
+        } now{(int)blockIdx.x, 0, item_of<T, P>(job, blockIdx.x, BN)}, next = now;
+        auto advance = [&](Cursor& c) {
+            if (++c.ks < c.it.stages) return;
             c.ks = 0;
             c.i += gridDim.x;
-            if (c.i >= job.items) return false;
-            c.it = item_of<P>(job, c.i, BN);
-            return true;
+            if (c.i < job.items) c.it = item_of<T, P>(job, c.i, BN);
         };
-        // addresses of a K-major A's rows, for the cursor that reads it
-        const T *arow[Lay::kAMn ? 1 : IA], *zrow[kDzA ? IA : 1];
-        auto set_rows = [&](const Item& it) {
-            if constexpr (!Lay::kAMn) {
+        int ring = 0;  // the stage's place among the kDepth in flight
+        constexpr int kChunkElems = 16 / sizeof(T);
+        // -- A that is converted. A warp serves the 32 TMEM lanes that it may write (its index mod 4) and, with 8
+        // warps, one half of the k; it copies just what it reads, so that no other warp has to be waited for.
+        constexpr int kHalf = 4 * K / W::kLoad;          // k of a warp
+        constexpr int kRowBytes = Lay::kAMn ? 32 * (int)sizeof(T) : kHalf * (int)sizeof(T);  // of its block
+        constexpr int kRows = Lay::kAMn ? kHalf : 32, kRowChunks = kRowBytes / 16;
+        constexpr int kBlock = kRows * kRowBytes;
+        const int quad = warp & 3, khalf = lw >> 2;
+        auto block_a = [&](int z) {  // (z = 1: the pre-activation's)
+            return smem + Lay::kOffRaw + ring * Lay::kRaw + z * Lay::kRawA + lw * kBlock;
+        };
+        auto chunk_a = [&](int r, int c) {  // chunk c of the block's row r: no two of 8 neighbouring rows in one bank
+            const int x = kRowChunks >= 8 ? r & 7 : kRowChunks == 4 ? (r >> 1) & 3 : 0;
+            return (uint32_t)(r * kRowBytes + (((c & ~7) | ((c ^ x) & 7)) << 4));
+        };
+        auto fetch_a = [&](const Cursor& c, const Operand& o, int z) {
+            constexpr int kPer = 32 / kRowChunks > 0 ? 32 / kRowChunks : 1;  // rows side by side in a warp's copies
+            constexpr int kCols = kRowChunks < 32 ? kRowChunks : 32;
+            const int kk = c.it.k0 + c.ks * K + khalf * kHalf;
+            const int row0 = Lay::kAMn ? kk : c.it.m0 + 32 * quad, col0 = Lay::kAMn ? c.it.m0 + 32 * quad : kk;
+            const int rlim = Lay::kAMn ? c.it.k1 : o.nrows;
+            unsigned char* blk = block_a(z);
+            copy_column<T, VEC, kRows / kPer, kPer>(
+                o, row0 + lane / kCols, rlim, col0 + (lane % kCols) * kChunkElems,
+                [&](int i) { return blk + chunk_a(lane / kCols + kPer * i, lane % kCols); });
+        };
+        auto convert_a = [&](int slot) {
+            constexpr int kB = 16;  // k at a time
+            const uint32_t col = tmem_a + ((uint32_t)(quad * 32) << 16) + slot * Lay::kACols + khalf * (kHalf / 2);
+            const unsigned char *blk = block_a(0), *zb = block_a(1);
 #pragma unroll
-                for (int i = 0; i < IA; ++i) {
-                    const int r = it.m0 + ShareA::row(lt, i);
-                    arow[i] = static_cast<const T*>(job.A.rows.p) + job.A.rows.offset(job.A.map, r) + 8 * ShareA::col(lt);
+            for (int b = 0; b < kHalf / kB; ++b) {
+                float v[kB];
+                if constexpr (Lay::kAMn) {
+                    // (float32) the lane's column, k after k
+#pragma unroll
+                    for (int j = 0; j < kB; ++j) {
+                        const int r = b * kB + j;
+                        v[j] = *reinterpret_cast<const float*>(blk + chunk_a(r, lane / 4) + 4 * (lane % 4));
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kB / kChunkElems; ++c)
+                        read16<T>(blk + chunk_a(lane, b * (kB / kChunkElems) + c), v + c * kChunkElems);
                     if constexpr (kDzA) {
-                        zrow[i] =
-                            static_cast<const T*>(job.Z.rows.p) + job.Z.rows.offset(job.Z.map, r) + 8 * ShareA::col(lt);
+                        if (job.silu) {
+                            float zv[kB];
+#pragma unroll
+                            for (int c = 0; c < kB / kChunkElems; ++c)
+                                read16<T>(zb + chunk_a(lane, b * (kB / kChunkElems) + c), zv + c * kChunkElems);
+#pragma unroll
+                            for (int j = 0; j < kB; ++j) v[j] *= silu_grad(zv[j]);
+                        }
+                    }
+                }
+                split_parts<T, kB>(v, [&](int p, const uint32_t(&w)[kB / 2]) {
+                    tc::tmem_st8(col + p * (K / 2) + b * (kB / 2), w);
+                });
+            }
+            tc::tmem_wait_st();
+        };
+        // -- B that is converted: units of 8 columns; a warp's 32 units of one index lie together in planes of their
+        // first and their second 16 bytes (one plane of bfloat16). The lanes copy the warp's units together, so
+        // that neighbouring lanes read neighbouring 16 bytes.
+        constexpr int kPlanes = sizeof(T) / 2;
+        auto unit_b = [&](int z, int i) {
+            return smem + Lay::kOffRaw + ring * Lay::kRaw + Lay::kRawA + (kDzA ? Lay::kRawZ : 0) + z * Lay::kRawB +
+                   (i * W::kLoad + lw) * (512 * kPlanes);
+        };
+        auto fetch_b = [&](const Cursor& c, const Operand& o, int z) {
+            const int kk = c.it.k0 + c.ks * K;
+            const int row0 = Lay::kBMn ? kk : c.it.n0, col0 = Lay::kBMn ? c.it.n0 : kk;
+            const int rlim = kDzB ? c.it.k1 : o.nrows;
+#pragma unroll
+            for (int h = 0; h < kPlanes; ++h) {
+                const int w = (lt & ~31) + 32 / kPlanes * h + lane / kPlanes, sub = lane % kPlanes;
+                const int lim = ShareB::kEven || ShareB::has(w, 0) ? rlim : 0;  // (one unit a thread at most then)
+                copy_column<T, VEC, ShareB::kIters, W::kLoaders / ShareB::kPerRow>(
+                    o, row0 + ShareB::row(w, 0), lim, col0 + 8 * ShareB::col(w) + sub * kChunkElems,
+                    [&](int i) { return unit_b(z, i) + sub * 512 + (32 / kPlanes * h + lane / kPlanes) * 16; });
+            }
+        };
+        float bsum[8];
+        auto convert_b = [&](unsigned char* sb) {
+#pragma unroll
+            for (int i = 0; i < ShareB::kIters; ++i) {
+                float v[8];
+#pragma unroll
+                for (int h = 0; h < kPlanes; ++h) read16<T>(unit_b(0, i) + h * 512 + lane * 16, v + h * kChunkElems);
+                if constexpr (kDzB) {
+                    if (job.silu) {
+                        float zv[8];
+#pragma unroll
+                        for (int h = 0; h < kPlanes; ++h)
+                            read16<T>(unit_b(1, i) + h * 512 + lane * 16, zv + h * kChunkElems);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] *= silu_grad(zv[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) bsum[j] += v[j];
+                }
+                if (ShareB::has(lt, i)) store_parts<T>(sb + ShareB::offset(lt, i), Lay::kBPart, v);
+            }
+        };
+        // -- operands used as they are, straight into the slot
+        auto copy_tile = [&](auto share_c, const Operand& o, unsigned char* dst, int row0, int rlim, int col0) {
+            using S = decltype(share_c);
+            const int lim = S::kEven || S::has(lt, 0) ? rlim : 0;
+            if (S::kEven || S::has(lt, 0))
+                copy_column<T, VEC, S::kIters, W::kLoaders / S::kPerRow>(o, row0 + S::row(lt, 0), lim,
+                                                                         col0 + 8 * S::col(lt),
+                                                                         [&](int i) { return dst + S::offset(lt, i); });
+        };
+        auto fetch = [&]() {  // the fetch cursor's stage, one group of copies
+            if (next.i < job.items) {
+                if constexpr (Lay::kTmemA) {
+                    fetch_a(next, job.A, 0);
+                    if constexpr (kDzA) {
+                        if (job.silu) fetch_a(next, job.Z, 1);
+                    }
+                }
+                if constexpr (Lay::kConvB) {
+                    fetch_b(next, job.B, 0);
+                    if constexpr (kDzB) {
+                        if (job.silu) fetch_b(next, job.Z, 1);
                     }
                 }
             }
-        };
-        // unit i of a stage's A (B) tile: its address, and how many of its elements exist
-        auto unit_a = [&](const Cursor& c, int i, const T*& p) {
-            const int kk = c.it.k0 + c.ks * kStageK;
-            if constexpr (Lay::kAMn) {
-                const int r = kk + ShareA::row(lt, i), col = c.it.m0 + 8 * ShareA::col(lt);
-                p = static_cast<const T*>(job.A.rows.p) + job.A.rows.offset(job.A.map, r) + col;
-                return r < c.it.k1 ? job.A.ncols - col : 0;
-            } else {
-                p = arow[i] + kk;
-                return c.it.m0 + ShareA::row(lt, i) < job.A.nrows ? job.A.ncols - kk - 8 * ShareA::col(lt) : 0;
-            }
-        };
-        auto unit_b = [&](const Cursor& c, int i, const T*& p, const T*& pz) {
-            const int kk = c.it.k0 + c.ks * kStageK;
-            const int r = (Lay::kBMn ? kk : c.it.n0) + ShareB::row(lt, i);
-            const int col = (Lay::kBMn ? c.it.n0 : kk) + 8 * ShareB::col(lt);
-            p = static_cast<const T*>(job.B.rows.p) + job.B.rows.offset(job.B.map, r) + col;
-            if (kDzB) pz = static_cast<const T*>(job.Z.rows.p) + job.Z.rows.offset(job.Z.map, r) + col;
-            return r < (kDzB ? c.it.k1 : job.B.nrows) ? job.B.ncols - col : 0;
-        };
-        auto fetch_a = [&](const Cursor& c, int h, int q) {  // unit q of part h (and its pre-activation)
-            if constexpr (kRegA) {
-                if (h * HA + q >= IA) return;
-                const T* p;
-                const int left = unit_a(c, h * HA + q, p);
-                ra[q].template load<VEC>(p, left);
-                if constexpr (kDzA) {
-                    if (job.silu) rz[q].template load<VEC>(zrow[h * HA + q] + c.it.k0 + c.ks * kStageK, left);
-                }
-            }
-        };
-        auto fetch_b = [&](const Cursor& c, int h, int q) {
-            if constexpr (kRegB) {
-                if (h * HB + q >= IB) return;
-                const T *p, *pz = nullptr;
-                const int left = unit_b(c, h * HB + q, p, pz);
-                rb[q].template load<VEC>(p, left);
-                if constexpr (kDzB) {
-                    if (job.silu) rz[q].template load<VEC>(pz, left);
-                }
-            }
-        };
-        auto dz = [&](float (&v)[8], const Unit<T>& z) {
-            if (!job.silu) return;
-            float zv[8];
-            z.get(zv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= silu_grad(zv[j]);
+            copy_commit();
+            advance(next);
         };
         auto arrive = [&](int slot) {  // this warp's part of the slot is written
             tc::fence_proxy_async();
+            if (Lay::kTmemA) tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&full[slot]);
         };
-        float bsum[8];
         int n = 0;
-        set_rows(now.it);
-#pragma unroll
-        for (int q = 0; q < HA; ++q) fetch_a(now, 0, q);
-#pragma unroll
-        for (int q = 0; q < HB; ++q) fetch_b(now, 0, q);
+        if constexpr (Lay::kRaw > 0) {
+            for (ring = 0; ring < Lay::kDepth; ++ring) fetch();
+            ring = 0;
+        }
         for (; now.i < job.items; ++n) {
-            const int slot = n % Lay::kSlots;
-            if (n >= Lay::kSlots && !wait(&empty[slot], (n / Lay::kSlots - 1) & 1)) break;
-            unsigned char* sa = smem + slot * Lay::kSlot;
-            unsigned char* sb = sa + NP * Lay::kAPart;
+            const int slot = n % kSlots;
+            if (n >= kSlots && !wait(&empty[slot], (n / kSlots - 1) & 1)) break;
+            if (Lay::kTmemA) tc::fence_after_sync();
+            unsigned char* sb = smem + slot * Lay::kSlot;
+            unsigned char* sa = sb + NP * Lay::kBPart;
             if (IMAGE && lt == 0) {
-                const int nks = (job.k + kStageK - 1) / kStageK;
+                const int nks = (job.k + K - 1) / K;
                 tc::mbar_expect_tx(&bfull[slot], NP * Lay::kBPart);
                 tc::bulk_g2s(sb, job.image + (size_t)((now.it.n0 / BN) * nks + now.ks) * (NP * Lay::kBPart),
                              NP * Lay::kBPart, &bfull[slot]);
                 images = n + 1;
             }
-            if constexpr (kCopyA) {
-#pragma unroll
-                for (int q = 0; q < IA; ++q) {
-                    const T* p;
-                    const int left = unit_a(now, q, p);
-                    copy16(sa + ShareA::offset(lt, q), left > 0 ? p : static_cast<const T*>(job.A.rows.p), left > 0);
-                }
+            const int kk = now.it.k0 + now.ks * K;
+            if constexpr (!Lay::kTmemA) {
+                copy_tile(ShareA{}, job.A, sa, Lay::kAMn ? kk : now.it.m0, Lay::kAMn ? now.it.k1 : job.A.nrows,
+                          Lay::kAMn ? now.it.m0 : kk);
             }
-            if constexpr (kCopyB) {
-#pragma unroll
-                for (int q = 0; q < IB; ++q) {
-                    const T *p, *pz = nullptr;
-                    const int left = unit_b(now, q, p, pz);
-                    copy16(sb + ShareB::offset(lt, q), left > 0 ? p : static_cast<const T*>(job.B.rows.p), left > 0);
-                }
+            if constexpr (Lay::kCopyB) {
+                copy_tile(ShareB{}, job.B, sb, Lay::kBMn ? kk : now.it.n0, job.B.nrows, Lay::kBMn ? now.it.n0 : kk);
             }
-            if (kCopies) copy_commit();
-            if (kDzB && now.ks == 0)
+            if constexpr (Lay::kRaw > 0) {
+                copy_wait<Lay::kDepth - 1>();
+                __syncwarp();
+                if constexpr (Lay::kTmemA) convert_a(slot);
+                if constexpr (Lay::kConvB) {
+                    if (kDzB && now.ks == 0)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) bsum[j] = 0.f;
-            // a unit's registers are refilled as soon as it is stored: it is in flight while the others are converted
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                const bool here = h + 1 < kHalves;
-                if (!here && advance(next) && kRegA) set_rows(next.it);
-                const bool more = next.i < job.items;
-                if constexpr (kRegA) {
-#pragma unroll
-                    for (int q = 0; q < HA; ++q) {
-                        if (h * HA + q < IA) {
-                            float v[8];
-                            ra[q].get(v);
-                            if constexpr (kDzA) {
-                                dz(v, rz[q]);
-                            }
-                            store_parts<T>(sa + ShareA::offset(lt, h * HA + q), Lay::kAPart, v);
-                        }
-                        if (here)
-                            fetch_a(now, h + 1, q);
-                        else if (more)
-                            fetch_a(next, 0, q);
-                    }
+                        for (int j = 0; j < 8; ++j) bsum[j] = 0.f;
+                    convert_b(sb);
                 }
-                if constexpr (kRegB) {
-#pragma unroll
-                    for (int q = 0; q < HB; ++q) {
-                        if (h * HB + q < IB) {
-                            float v[8];
-                            rb[q].get(v);
-                            if constexpr (kDzB) {
-                                dz(v, rz[q]);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) bsum[j] += v[j];
-                            }
-                            store_parts<T>(sb + ShareB::offset(lt, h * HB + q), Lay::kBPart, v);
-                        }
-                        if (here)
-                            fetch_b(now, h + 1, q);
-                        else if (more)
-                            fetch_b(next, 0, q);
-                    }
-                }
+                __syncwarp();  // read by all lanes
+                fetch();       // its group takes in the copies into the slot
+                ring = ring + 1 == Lay::kDepth ? 0 : ring + 1;
+            } else {
+                copy_commit();
             }
-            if (!kCopies) {
+            if constexpr (Lay::kLag == 0) {
                 arrive(slot);
-            } else if (n >= kDepth) {
-                copy_wait<kDepth>();
-                arrive((n - kDepth) % Lay::kSlots);
+            } else if (n >= Lay::kLag) {
+                if (Lay::kRaw == 0) copy_wait<Lay::kLag>();  // else the wait above has passed that stage's copies
+                arrive((n - Lay::kLag) % kSlots);
             }
             if (kDzB && now.ks + 1 >= now.it.stages && job.bias_part && now.it.m0 == 0) {
                 // the item's sums of dz over its rows: the lanes of a warp that share columns, one row per warp
@@ -633,7 +725,7 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                 for (int j = 0; j < 8; ++j)
                     for (int o = ShareB::kPerRow; o < 32; o <<= 1) bsum[j] += __shfl_xor_sync(0xffffffffu, bsum[j], o);
                 if (lane < ShareB::kPerRow) {
-                    float* row = job.bias_part + (size_t)(now.it.split * kLoadWarps + (warp - kEpiWarps)) * job.n;
+                    float* row = job.bias_part + (size_t)(now.it.split * W::kLoad + lw) * job.n;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int c = now.it.n0 + 8 * ShareB::col(lt) + j;
@@ -641,54 +733,60 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                     }
                 }
             }
-            now = next;
-            if (kCopyA && now.ks == 0) set_rows(now.it);
+            advance(now);
         }
-        if (kCopies) {
-            copy_wait<0>();
-            for (int m = n > kDepth ? n - kDepth : 0; m < n; ++m) arrive(m % Lay::kSlots);
-        }
-    } else if (warp == kMmaWarp && lane == 0) {
-        constexpr uint32_t idesc = idesc_bf16<Lay::kAMn, Lay::kBMn>(BN);
+        copy_wait<0>();
+        for (int m = n > Lay::kLag ? n - Lay::kLag : 0; m < n; ++m) arrive(m % kSlots);
+    } else if (warp == W::kMma && lane == 0) {
+        constexpr uint32_t idesc = idesc_bf16<Lay::kAMn && !Lay::kTmemA, Lay::kBMn>(BN);
         // one K step of 16, one part: descriptor units of 16 bytes
         constexpr uint32_t kStepA = (Lay::kAMn ? 2048 : 32) >> 4, kStepB = (Lay::kBMn ? 2048 : 32) >> 4;
         constexpr int kPairs = NP == 3 ? 6 : 1;
         constexpr int pa[6] = {NP == 3 ? 1 : 0, 0, 2, 0, 1, 0}, pb[6] = {NP == 3 ? 1 : 0, 2, 0, 1, 0, 0};
-        const uint64_t base_a = desc128<Lay::kAMn>(tc::smem_u32(smem));
-        const uint64_t base_b = desc128<Lay::kBMn>(tc::smem_u32(smem + NP * Lay::kAPart));
-        // the stage's MMAs, unrolled: descriptors are the slot's plus constants
-        auto issue = [&](auto steps_c, uint32_t d, uint64_t da, uint64_t db, bool first) {
+        uint64_t base_a = 0;
+        if constexpr (!Lay::kTmemA) base_a = operand_desc<Lay::kAMn, K>(tc::smem_u32(smem + NP * Lay::kBPart));
+        const uint64_t base_b = operand_desc<Lay::kBMn, K>(tc::smem_u32(smem));
+        // the stage's MMAs, unrolled: operand addresses are the slot's plus constants
+        auto issue = [&](auto steps_c, uint32_t d, int slot, bool first) {
             constexpr int S = decltype(steps_c)::value;
+            const uint64_t db = base_b + (uint64_t)(slot * (Lay::kSlot >> 4));
+            [[maybe_unused]] const uint64_t da = base_a + (uint64_t)(slot * (Lay::kSlot >> 4));
+            [[maybe_unused]] const uint32_t ta = tmem_a + slot * Lay::kACols;
 #pragma unroll
             for (int q = 0; q < kPairs; ++q)
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    mma_bf16(d, da + (uint64_t)(pa[q] * (Lay::kAPart >> 4) + s * kStepA),
-                             db + (uint64_t)(pb[q] * (Lay::kBPart >> 4) + s * kStepB), idesc,
-                             q == 0 && s == 0 ? (first ? 0u : 1u) : 1u);
+                for (int s = 0; s < S; ++s) {
+                    const uint32_t acc = q == 0 && s == 0 ? (first ? 0u : 1u) : 1u;
+                    const uint64_t b = db + (uint64_t)(pb[q] * (Lay::kBPart >> 4) + s * kStepB);
+                    if constexpr (Lay::kTmemA)
+                        mma_bf16_ta(d, ta + pa[q] * (K / 2) + s * 8, b, idesc, acc);
+                    else
+                        mma_bf16(d, da + (uint64_t)(s * kStepA), b, idesc, acc);
+                }
         };
         int n = 0, chunk = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
-            const Item it = item_of<P>(job, i, BN);
+            const Item it = item_of<T, P>(job, i, BN);
             for (int ks = 0; ks < it.stages; ++ks, ++n) {
-                const int slot = n % Lay::kSlots, buf = chunk % kRing;
+                const int slot = n % kSlots, buf = chunk % kRing;
                 const bool first = ks % kChunk<T> == 0;
                 if ((first && chunk >= kRing && !wait1(&tempty[buf], (chunk / kRing - 1) & 1)) ||
-                    !wait1(&full[slot], (n / Lay::kSlots) & 1) ||
-                    (IMAGE && !wait1(&bfull[slot], (n / Lay::kSlots) & 1))) {
+                    !wait1(&full[slot], (n / kSlots) & 1) || (IMAGE && !wait1(&bfull[slot], (n / kSlots) & 1))) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                const int left = it.k1 - it.k0 - ks * kStageK;
+                const int left = it.k1 - it.k0 - ks * K;
                 const uint32_t d = tmem + buf * BN;
-                const uint64_t da = base_a + (uint64_t)(slot * (Lay::kSlot >> 4));
-                const uint64_t db = base_b + (uint64_t)(slot * (Lay::kSlot >> 4));
-                if (left > 48) issue(Int<4>{}, d, da, db, first);
-                else if (left > 32) issue(Int<3>{}, d, da, db, first);
-                else if (left > 16) issue(Int<2>{}, d, da, db, first);
-                else issue(Int<1>{}, d, da, db, first);
+                if (left > K - 16)
+                    issue(Int<K / 16>{}, d, slot, first);
+                else if (K == 64 && left > 32)
+                    issue(Int<K == 64 ? 3 : 1>{}, d, slot, first);
+                else if (K == 64 && left > 16)
+                    issue(Int<K == 64 ? 2 : 1>{}, d, slot, first);
+                else
+                    issue(Int<1>{}, d, slot, first);
                 tc::mma_commit(&empty[slot]);
                 if (ks + 1 == it.stages || (ks + 1) % kChunk<T> == 0) {
                     tc::mma_commit(&tfull[buf]);
@@ -696,15 +794,15 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                 }
             }
         }
-    } else if (warp < kEpiWarps) {
-        constexpr int NR = BN / 4;  // registers of a warp's 16 lanes x BN / 2 columns
+    } else if (warp < W::kEpi) {
+        constexpr int kCols = 4 * BN / W::kEpi, NR = kCols / 2;  // columns of a warp; registers of its 16 lanes
         constexpr int kPiece = NR < 16 ? NR : 16;
-        const int quad = warp & 3, half = warp >> 2;
-        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
+        const int quad = warp & 3, part = warp >> 2;
+        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
         int chunk = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
-            const Item it = item_of<P>(job, i, BN);
+            const Item it = item_of<T, P>(job, i, BN);
             float acc[2][NR];
 #pragma unroll
             for (int j = 0; j < NR; ++j) acc[0][j] = acc[1][j] = 0.f;
@@ -723,44 +821,50 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                         tc::tmem_ld_frag<kPiece>(base + ((uint32_t)(16 * h) << 16) + buf * BN + 2 * c, v);
                         tc::tmem_wait_ld(v);
 #pragma unroll
-                        for (int j = 0; j < kPiece; ++j) acc[h][c + j] += v[j];
+                        for (int j = 0; j < kPiece; j += 2) {
+                            const float2 a = __fadd2_rn(make_float2(acc[h][c + j], acc[h][c + j + 1]),
+                                                        make_float2(v[j], v[j + 1]));
+                            acc[h][c + j] = a.x, acc[h][c + j + 1] = a.y;
+                        }
                     }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&tempty[buf]);
             }
             if (!ok) break;
-            if (job.vec_out)
-                finish<T, P, BN, true>(job, it, acc, quad, half, lane);
+            if (job.vec_out && job.map.per.d == 1 && it.m0 + kRowsTile <= job.m && it.n0 + BN <= job.n)
+                finish<T, P, kCols, Pairs::kFull>(job, it, acc, quad, part, lane);
+            else if (job.vec_out)
+                finish<T, P, kCols, Pairs::kEven>(job, it, acc, quad, part, lane);
             else
-                finish<T, P, BN, false>(job, it, acc, quad, half, lane);
+                finish<T, P, kCols, Pairs::kAny>(job, it, acc, quad, part, lane);
         }
     }
     __syncthreads();
     if (*abort_flag) {  // leave no MMA or copy in flight on the freed memory
-        if (t == 32 * kMmaWarp) {
+        if (t == 32 * W::kMma) {
             atomicOr(&g_fault, 1);
             tc::mma_commit(drain);
             tc::mbar_wait(drain, 0, kWaitLimit);
         }
-        if (IMAGE && t == 32 * kEpiWarps)
-            for (int m = images > Lay::kSlots ? images - Lay::kSlots : 0; m < images; ++m)
-                tc::mbar_wait(&bfull[m % Lay::kSlots], (m / Lay::kSlots) & 1, kWaitLimit);
+        if (IMAGE && t == 32 * W::kEpi)
+            for (int m = images > kSlots ? images - kSlots : 0; m < images; ++m)
+                tc::mbar_wait(&bfull[m % kSlots], (m / kSlots) & 1, kWaitLimit);
         __syncthreads();
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, Lay::kTmemCols);
+    if (warp == W::kMma) tc::tmem_dealloc(tmem, Lay::kTmemCols);
 }
 
 // W as tiles of operand parts in the layout of a slot's B, tile (nt, ks) after tile:
 // converted once here instead of once per row tile by every CTA. A thread converts
 // units of 8 consecutive elements of W.
 template <typename T, Product P, int BN>
-__global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restrict__ W, int rows, int cols, bool vec,
+__global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restrict__ W, int rows, int cols,
                                                                unsigned char* __restrict__ image) {
-    using Lay = Layout<T, P, BN>;
-    constexpr int R = Lay::kBMn ? kStageK : BN, C = Lay::kBMn ? BN : kStageK;  // W's rows and columns in a tile
+    using Lay = Layout<T, P, BN, true, true>;
+    constexpr int R = Lay::kBMn ? Lay::kK : BN, C = Lay::kBMn ? BN : Lay::kK;  // W's rows and columns in a tile
     constexpr int kPerRow = C / 8, kUnits = R * kPerRow;
     const int ct = (cols + C - 1) / C, rt = (rows + R - 1) / R;
     const int u = blockIdx.x * 256 + threadIdx.x, tile = u / kUnits, w = u % kUnits;
@@ -770,16 +874,11 @@ __global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restri
     const int r = w / kPerRow, c = w % kPerRow, gr = rti * R + r, gc = cti * C + 8 * c;
     const T* p = W + (size_t)gr * cols + gc;
     const int left = gr < rows ? cols - gc : 0;
-    Unit<T> q;
-    if (vec)
-        q.template load<true>(p, left);
-    else
-        q.template load<false>(p, left);
     float v[8];
-    q.get(v);
-    store_parts<T>(image + (size_t)tile * kParts<T> * Lay::kBPart + (uint32_t)(c >> 3) * kPanel +
-                       (uint32_t)(r >> 3) * 1024 + (uint32_t)(r & 7) * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4),
-                   Lay::kBPart, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? to_float(p[j]) : 0.f;
+    store_parts<T>(image + (size_t)tile * kParts<T> * Lay::kBPart + chunk_offset<Lay::kK>(r, c), Lay::kBPart,
+                   v);
 }
 
 // grad_W from the ranges' sums [splits][count] and grad_bias from [bias_rows][N], both in
@@ -830,7 +929,7 @@ Operand matrix(const void* p, int nrows, int ncols, int elem) {
 
 template <typename T, Product P, int BN, bool VEC, bool IMAGE>
 cudaError_t launch_kernel(const Job& j, cudaStream_t s) {
-    using Lay = Layout<T, P, BN>;
+    using Lay = Layout<T, P, BN, VEC, IMAGE>;
     const cudaError_t e = cudaFuncSetAttribute(etp_linear_kernel<T, P, BN, VEC, IMAGE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kBytes);
     if (e != cudaSuccess) return e;
@@ -845,12 +944,12 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
     const bool z = !j.Z.rows.p || j.Z.vec;
     if constexpr (P != Product::kGradW) {
         if (image) {
-            using Lay = Layout<T, P, BN>;
+            using Lay = Layout<T, P, BN, true, true>;
             const int rows = j.B.nrows, cols = j.B.ncols;
-            const int R = Lay::kBMn ? kStageK : BN, C = Lay::kBMn ? BN : kStageK;
+            const int R = Lay::kBMn ? Lay::kK : BN, C = Lay::kBMn ? BN : Lay::kK;
             const long long units = (long long)((rows + R - 1) / R) * ((cols + C - 1) / C) * (R * C / 8);
             etp_linear_image_kernel<T, P, BN><<<(unsigned)((units + 255) / 256), 256, 0, s>>>(
-                static_cast<const T*>(j.B.rows.p), rows, cols, j.B.vec, image);
+                static_cast<const T*>(j.B.rows.p), rows, cols, image);
             const cudaError_t e = cudaGetLastError();
             if (e != cudaSuccess) return e;
             j.image = image;
@@ -864,7 +963,7 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
 
 // How the forward and grad_x products of M rows, k contracted and n output columns are
 // tiled: the widest tile that still gives every SM one, or the narrowest; and whether W
-// is converted ahead (an image), which pays once several row tiles share it.
+// is converted ahead (an image), which pays once a CTA would convert it more than once.
 struct Tiling {
     int bn;
     bool image;
@@ -875,23 +974,22 @@ Tiling tiling(bool bf16, Product p, int M, int k, int n) {
     const int sms = sm_count();
     Tiling t;
     t.bn = n > 64 && mt * ((n + 127) / 128) >= sms ? 128 : n > 32 && mt * ((n + 63) / 64) >= sms ? 64 : 32;
-    t.image = mt >= sms;
-    const size_t part = (size_t)(p == Product::kForward && t.bn < 64 ? 64 : t.bn) * kStageK * 2;
-    t.image_bytes =
-        t.image ? (size_t)((n + t.bn - 1) / t.bn) * ((k + kStageK - 1) / kStageK) * (bf16 ? 1 : 3) * part : 0;
+    t.image = mt * ((n + t.bn - 1) / t.bn) >= 2 * sms;
+    constexpr int K = 64;  // k of a stage of either
+    static_assert(kStageK<float, Product::kForward> == K && kStageK<float, Product::kGradX> == K, "image tiles");
+    const size_t part = (size_t)(p == Product::kForward && t.bn < 64 ? 64 : t.bn) * K * 2;
+    t.image_bytes = t.image ? (size_t)((n + t.bn - 1) / t.bn) * ((k + K - 1) / K) * (bf16 ? 1 : 3) * part : 0;
     return t;
 }
 
 template <typename T, Product P>
 cudaError_t launch(Job& j, int bn, int splits, unsigned char* image, cudaStream_t s) {
-    j.ntn = (j.n + bn - 1) / bn;
-    const long long tiles = (long long)((j.m + kRowsTile - 1) / kRowsTile) * j.ntn;
-    if (tiles > 0x7fff0000LL) return cudaErrorInvalidValue;
-    j.tiles = j.items = (int)tiles;
-    if (P == Product::kGradW) {  // a tile of no rows still is one tile
-        if (j.m == 0) j.tiles = j.ntn;
-        j.items = j.tiles * splits;
-    }
+    j.ntn = FastDiv((j.n + bn - 1) / bn);
+    const int mtn = P == Product::kGradW && j.m == 0 ? 1 : (j.m + kRowsTile - 1) / kRowsTile;  // no rows: still a tile
+    const long long tiles = (long long)mtn * j.ntn.d;
+    if (tiles * splits > 0x7fff0000LL) return cudaErrorInvalidValue;
+    j.tiles = FastDiv((int)tiles);
+    j.items = (int)tiles * splits;
     switch (bn) {
         case 128: return launch_bn<T, P, 128>(j, image, s);
         case 64: return launch_bn<T, P, 64>(j, image, s);
@@ -909,12 +1007,12 @@ Ranges ranges(int M, int K, int N) {
     r.bn = N > 64 ? 128 : N > 32 ? 64 : 32;
     r.tiles = ((K + kRowsTile - 1) / kRowsTile) * ((N + r.bn - 1) / r.bn);
     const int sms = sm_count();
-    const int stages = (M + kStageK - 1) / kStageK;
+    const int stages = (M + kRangeK - 1) / kRangeK;
     int want = r.tiles < sms ? sms / r.tiles : 1;
     const int most = (stages + 3) / 4;
     want = want < most ? want : most;
     const int per = want > 0 ? (stages + want - 1) / want : 1;
-    r.range = per * kStageK;
+    r.range = per * kRangeK;
     r.splits = stages > 0 ? (stages + per - 1) / per : 0;
     return r;
 }
