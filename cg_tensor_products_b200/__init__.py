@@ -18,6 +18,7 @@ The dense row operators (include/etp_dense.h) need no plan; they read blocks of 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -84,7 +85,7 @@ def _load():
         "etp_forward_ordered": [vp, i32, i32] + [vp] * 10 + [sz, vp],
         "etp_backward_ordered": [vp, i32, i32] + [vp] * 13 + [sz, vp],
         "etp_linear_forward": [i32] * 5 + [vp, vp, vp, i32, vp, vp, vp, vp, sz, vp],
-        "etp_linear_workspace_size": [i32] * 5 + [ctypes.POINTER(sz)],
+        "etp_linear_workspace_size": [i32] * 6 + [ctypes.POINTER(sz)],
         "etp_linear_backward": [i32] * 5 + [vp, vp, i32] + [vp] * 6 + [sz, vp],
         "etp_layer_norm_forward": [i32] * 4 + [ctypes.c_float] + [vp] * 7,
         "etp_layer_norm_workspace_size": [i32] * 4 + [ctypes.POINTER(sz)],
@@ -447,21 +448,20 @@ def _dense_rows(t, name: str, like=None, channels=None):
     like: the tensor whose leading sizes and dtype it must share; channels: its C."""
     if t is None:
         return None
-    shape = t.shape
+    shape, st = t.shape, t.stride()
     nd = len(shape)
     if nd != 2 and nd != 3:
         raise ValueError(f"{name}: expected [rows, channels] or [groups, rows, channels], got {tuple(shape)}")
     if like is not None:
-        if t.dtype != like.dtype:
+        if t.dtype is not like.dtype:
             raise ValueError(f"{name}: expected {like.dtype}, got {t.dtype}")
         if shape[:-1] != like.shape[:-1]:
             raise ValueError(f"{name}: expected leading sizes {tuple(like.shape[:-1])}, got {tuple(shape[:-1])}")
     if channels is not None and shape[-1] != channels:
         raise ValueError(f"{name}: expected {channels} channels, got {shape[-1]}")
-    st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: channels must be contiguous (stride {st[-1]})")
-    return _Rows(t.data_ptr(), st[0], st[1] if nd == 3 else 0)
+    return ctypes.byref(_Rows(t.data_ptr(), st[0], st[1] if nd == 3 else 0))
 
 
 def _dense_type(x):
@@ -472,28 +472,72 @@ def _dense_type(x):
 
 
 def _dense_vector(t, name: str, like, *shape):
+    """Address of a contiguous tensor of like's dtype and the given shape (None for None)."""
     if t is None:
         return None
-    if t.dtype != like.dtype or tuple(t.shape) != shape:
+    if t.dtype is not like.dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {like.dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _dense_device(*ts):
-    """The one CUDA device of the given tensors (None entries are skipped); strided rows are accepted."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors: this library has no CPU path")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices ({dev}, {t.device})")
-    return dev
+def _dense_device(x, *ts):
+    """Index of the CUDA device of x, which the other tensors (None entries are skipped) must share."""
+    index = x.get_device()
+    for t in (x, *ts):
+        if t is not None:
+            at = t.get_device()
+            if at < 0:
+                raise ValueError("tensors must be CUDA tensors: this library has no CPU path")
+            if at != index:
+                raise ValueError(f"tensors on different devices ({x.device}, {t.device})")
+    return index
+
+
+def _dense_call(index: int, where: str, fn, *args, stream=None):
+    """fn(*args, stream) with device `index` current, on torch's current stream of it or the caller's."""
+    import torch
+
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device.index != index:
+            raise ValueError(f"{where}: stream on {stream.device}, tensors on cuda:{index}")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == index:  # switching costs more than a small launch
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != ETP_OK:
+        raise EtpError(status, where)
+
+
+@functools.lru_cache(maxsize=1024)
+def _dense_bytes(index: int, name: str, *args) -> int:
+    """Bytes that the size function `name` answers for these sizes on device `index` (they depend on nothing else)."""
+    import torch
+
+    b = ctypes.c_size_t()
+    with torch.cuda.device(index):
+        _check(getattr(_load(), name)(*args, ctypes.byref(b)), name)
+    return b.value
+
+
+def _dense_workspace(index: int, workspace, name: str, *args):
+    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any."""
+    if workspace is not None:
+        _expect(workspace, "workspace", "uint8", (None,))
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        return workspace, workspace.numel()
+    n = _dense_bytes(index, name, *args)
+    if n == 0:
+        return None, 0
+    import torch
+
+    return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
 
 
 def _span(t):
@@ -532,12 +576,6 @@ def _dense_outputs(outs, ins, in_place=()):
                 raise ValueError(f"{n} must not overlap {m}")
 
 
-def _check_workspace(workspace):
-    _expect(workspace, "workspace", "uint8", (None,))
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-
-
 def _dense_shape(x):
     """(groups, per_group) of x's rows."""
     return (x.shape[0], 1) if x.dim() == 2 else (x.shape[0], x.shape[1])
@@ -551,31 +589,13 @@ def _check_linear(x, W, activation):
     return _ACTIVATIONS[activation]
 
 
-def linear_workspace_size(M: int, K: int, N: int, dtype="float32", device=None) -> int:
-    """Bytes of workspace linear_forward and linear_backward need for M rows (etp_linear_workspace_size on `device`)."""
+def linear_workspace_size(M: int, K: int, N: int, dtype="float32", backward: bool = False, device=None) -> int:
+    """Bytes of workspace linear_forward (linear_backward) needs for M rows (etp_linear_workspace_size on `device`)."""
     import torch
 
-    b = ctypes.c_size_t()
-    code = _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")]
-    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        _check(_load().etp_linear_workspace_size(code, int(M), 1, int(K), int(N), ctypes.byref(b)),
-               "etp_linear_workspace_size")
-    return b.value
-
-
-def _linear_workspace(code, groups, per, K, N, workspace, dev):
-    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any."""
-    import torch
-
-    if workspace is not None:
-        _check_workspace(workspace)
-        return workspace, workspace.numel()
-    b = ctypes.c_size_t()
-    with torch.cuda.device(dev):
-        _check(_load().etp_linear_workspace_size(code, groups, per, K, N, ctypes.byref(b)), "etp_linear_workspace_size")
-    if b.value == 0:
-        return None, 0
-    return torch.empty(b.value, dtype=torch.uint8, device=dev), b.value
+    index = torch.device(device).index if device is not None else torch.cuda.current_device()
+    return _dense_bytes(index, "etp_linear_workspace_size", _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")],
+                        int(M), 1, int(K), int(N), int(bool(backward)))
 
 
 def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=False, z=None, out=None,
@@ -585,29 +605,25 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     for all. activation: 'none' or 'silu'. save_z=True (or z given) also keeps z = x W + bias for linear_backward:
     returns (out, z). out may be residual itself. workspace: uint8 device tensor of linear_workspace_size bytes
     (allocated when None)."""
-    import torch
-
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
     K, N = W.shape
     xr = _dense_rows(x, "x", None, K)
-    Wp = _dense_vector(W, "W", x, K, N)
-    bp = _dense_vector(bias, "bias", x, N)
+    Wp, bp = _dense_vector(W, "W", x, K, N), _dense_vector(bias, "bias", x, N)
     rr = _dense_rows(residual, "residual", x, N)
     if out is not None or z is not None:
         _dense_outputs([("out", out), ("z", z)], [("x", x), ("W", W), ("bias", bias), ("residual", residual)],
                        {("out", "residual")})
     if out is None:
-        out = torch.empty((*x.shape[:-1], N), device=x.device, dtype=x.dtype)
+        out = x.new_empty((*x.shape[:-1], N))
     if z is None and save_z:
-        z = torch.empty((*x.shape[:-1], N), device=x.device, dtype=x.dtype)
+        z = x.new_empty((*x.shape[:-1], N))
     orow, zr = _dense_rows(out, "out", x, N), _dense_rows(z, "z", x, N)
-    dev = _dense_device(x, W, bias, residual, z, out, workspace)
+    index = _dense_device(x, W, bias, residual, z, out, workspace)
     groups, per = _dense_shape(x)
-    workspace, nbytes = _linear_workspace(code, groups, per, K, N, workspace, dev)
-    _launch(dev, "etp_linear_forward", _load().etp_linear_forward, code, groups, per, K, N, ctypes.byref(xr), Wp,
-            bp, act, rr and ctypes.byref(rr), zr and ctypes.byref(zr), ctypes.byref(orow), _ptr(workspace), nbytes,
-            stream=stream)
+    workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 0)
+    _dense_call(index, "etp_linear_forward", _load().etp_linear_forward, code, groups, per, K, N, xr, Wp, bp, act, rr,
+                zr, orow, _ptr(workspace), nbytes, stream=stream)
     return out if z is None else (out, z)
 
 
@@ -615,8 +631,6 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
                     grad_bias=None, workspace=None, stream=None):
     """(grad_x, grad_W, grad_bias) of linear_forward for the cotangent grad_out (launches etp_linear_backward);
     unwanted ones are None. z: what linear_forward kept (needed for 'silu'). The residual's gradient is grad_out."""
-    import torch
-
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
     K, N = W.shape
@@ -630,19 +644,18 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
         _dense_outputs([("grad_x", grad_x), ("grad_W", grad_W), ("grad_bias", grad_bias)],
                        [("x", x), ("W", W), ("grad_out", grad_out), ("z", z)])
     if "x" in want and grad_x is None:
-        grad_x = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+        grad_x = x.new_empty(x.shape)
     if "W" in want and grad_W is None:
-        grad_W = torch.empty((K, N), device=x.device, dtype=x.dtype)
+        grad_W = x.new_empty((K, N))
     if "bias" in want and grad_bias is None:
-        grad_bias = torch.empty(N, device=x.device, dtype=x.dtype)
+        grad_bias = x.new_empty(N)
     gxr = _dense_rows(grad_x, "grad_x", x, K)
     gWp, gbp = _dense_vector(grad_W, "grad_W", x, K, N), _dense_vector(grad_bias, "grad_bias", x, N)
-    dev = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
+    index = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
     groups, per = _dense_shape(x)
-    workspace, nbytes = _linear_workspace(code, groups, per, K, N, workspace, dev)
-    _launch(dev, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, ctypes.byref(xr), Wp, act,
-            zr and ctypes.byref(zr), ctypes.byref(gr), gxr and ctypes.byref(gxr), gWp, gbp, _ptr(workspace),
-            nbytes, stream=stream)
+    workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 1)
+    _dense_call(index, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, xr, Wp, act, zr, gr,
+                gxr, gWp, gbp, _ptr(workspace), nbytes, stream=stream)
     return grad_x, grad_W, grad_bias
 
 
@@ -653,39 +666,40 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     import torch
 
     code = _dense_type(x)
-    C = x.shape[-1] if x.dim() else 0
     xr = _dense_rows(x, "x")
+    lead, C = x.shape[:-1], x.shape[-1]
     wp, bp = _dense_vector(weight, "weight", x, C), _dense_vector(bias, "bias", x, C)
     if out is not None or mean is not None or rstd is not None:
         _dense_outputs([("out", out), ("mean", mean), ("rstd", rstd)], [("x", x), ("weight", weight), ("bias", bias)],
                        {("out", "x")})
     if out is None:
-        out = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+        out = x.new_empty(x.shape)
     if mean is None:
-        mean = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+        mean = x.new_empty(lead, dtype=torch.float32)
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+        rstd = x.new_empty(lead, dtype=torch.float32)
     orow = _dense_rows(out, "out", x, C)
+    _check_moments(x, mean, rstd)
+    index = _dense_device(x, weight, bias, out, mean, rstd)
+    _dense_call(index, "etp_layer_norm_forward", _load().etp_layer_norm_forward, code, *_dense_shape(x), C, float(eps),
+                xr, wp, bp, orow, mean.data_ptr(), rstd.data_ptr(), stream=stream)
+    return out, mean, rstd
+
+
+def _check_moments(x, mean, rstd):
     for t, name in ((mean, "mean"), (rstd, "rstd")):
         _expect(t, name, "float32", tuple(x.shape[:-1]))
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous")
-    dev = _dense_device(x, weight, bias, out, mean, rstd)
-    _launch(dev, "etp_layer_norm_forward", _load().etp_layer_norm_forward, code, *_dense_shape(x), C, float(eps),
-            ctypes.byref(xr), wp, bp, ctypes.byref(orow), _ptr(mean), _ptr(rstd), stream=stream)
-    return out, mean, rstd
 
 
 def layer_norm_workspace_size(M: int, C: int, dtype="float32", device=None) -> int:
     """Bytes of workspace layer_norm_backward needs for M rows (etp_layer_norm_workspace_size on `device`)."""
     import torch
 
-    b = ctypes.c_size_t()
-    code = _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")]
-    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        _check(_load().etp_layer_norm_workspace_size(code, int(M), 1, int(C), ctypes.byref(b)),
-               "etp_layer_norm_workspace_size")
-    return b.value
+    index = torch.device(device).index if device is not None else torch.cuda.current_device()
+    return _dense_bytes(index, "etp_layer_norm_workspace_size",
+                        _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")], int(M), 1, int(C))
 
 
 def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "bias"), grad_x=None, grad_weight=None,
@@ -693,37 +707,32 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
     """(grad_x, grad_weight, grad_bias) of layer_norm_forward for the cotangent grad_out (launches
     etp_layer_norm_backward); unwanted ones are None. weight: as in the forward (None: ones); mean, rstd: what it
     returned. grad_x may be grad_out or x itself."""
-    import torch
-
     code = _dense_type(x)
-    C = x.shape[-1] if x.dim() else 0
-    xr, gr = _dense_rows(x, "x"), _dense_rows(grad_out, "grad_out", x, C)
+    xr = _dense_rows(x, "x")
+    C = x.shape[-1]
+    gr = _dense_rows(grad_out, "grad_out", x, C)
     wp = _dense_vector(weight, "weight", x, C)
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _expect(t, name, "float32", tuple(x.shape[:-1]))
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
+    _check_moments(x, mean, rstd)
     if grad_x is not None or grad_weight is not None or grad_bias is not None:
         _dense_outputs([("grad_x", grad_x), ("grad_weight", grad_weight), ("grad_bias", grad_bias)],
                        [("x", x), ("weight", weight), ("mean", mean), ("rstd", rstd), ("grad_out", grad_out)],
                        {("grad_x", "x"), ("grad_x", "grad_out")})
     if "x" in want and grad_x is None:
-        grad_x = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+        grad_x = x.new_empty(x.shape)
     if "weight" in want and grad_weight is None:
-        grad_weight = torch.empty(C, device=x.device, dtype=x.dtype)
+        grad_weight = x.new_empty(C)
     if "bias" in want and grad_bias is None:
-        grad_bias = torch.empty(C, device=x.device, dtype=x.dtype)
+        grad_bias = x.new_empty(C)
     gxr = _dense_rows(grad_x, "grad_x", x, C)
     gwp, gbp = _dense_vector(grad_weight, "grad_weight", x, C), _dense_vector(grad_bias, "grad_bias", x, C)
-    dev = _dense_device(x, weight, mean, rstd, grad_out, grad_x, grad_weight, grad_bias, workspace)
+    index = _dense_device(x, weight, mean, rstd, grad_out, grad_x, grad_weight, grad_bias, workspace)
     groups, per = _dense_shape(x)
-    if workspace is None and (grad_weight is not None or grad_bias is not None):
-        workspace = torch.empty(max(layer_norm_workspace_size(groups * per, C, x.dtype, dev), 16), dtype=torch.uint8,
-                                device=dev)
-    _check_workspace(workspace)
-    _launch(dev, "etp_layer_norm_backward", _load().etp_layer_norm_backward, code, groups, per, C, ctypes.byref(xr), wp,
-            _ptr(mean), _ptr(rstd), ctypes.byref(gr), gxr and ctypes.byref(gxr), gwp, gbp, _ptr(workspace),
-            0 if workspace is None else workspace.numel(), stream=stream)
+    nbytes = 0
+    if grad_weight is not None or grad_bias is not None:
+        workspace, nbytes = _dense_workspace(index, workspace, "etp_layer_norm_workspace_size", code, groups, per, C)
+    _dense_call(index, "etp_layer_norm_backward", _load().etp_layer_norm_backward, code, groups, per, C, xr, wp,
+                mean.data_ptr(), rstd.data_ptr(), gr, gxr, gwp, gbp, _ptr(workspace) if nbytes else None, nbytes,
+                stream=stream)
     return grad_x, grad_weight, grad_bias
 
 

@@ -110,6 +110,27 @@ __device__ __forceinline__ float silu_grad(float z) {
     return s * fmaf(z, 1.f - s, 1.f);
 }
 
+// Programmatic dependent launch: a kernel launched by launch_after may start once every
+// block of the kernel before it on the stream has called launch_dependents (or ended), and
+// calls wait_for_previous before it reads that kernel's results or writes anything. Its
+// launch overlaps with the other's run.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int blocks, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 int sm_count();  // multiprocessors of the current device
 
 // Launches (arguments checked by the C ABI). V16: every row of every operand and every

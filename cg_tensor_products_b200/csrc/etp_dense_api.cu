@@ -2,6 +2,7 @@
 // argument checks and launches on the caller's stream.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -11,12 +12,20 @@ namespace etp {
 namespace dense {
 
 int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    // a device's multiprocessors do not change; 0: not asked for yet
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return 148;
     }
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 148;
+    }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -121,15 +130,20 @@ etp_status etp_linear_forward(etp_dtype dtype, int groups, int per_group, int K,
     return cuda_status(etp::dense::linear_forward(dtype == ETP_BF16, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group, int K, int N, size_t* bytes) {
+etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group, int K, int N, int backward,
+                                     size_t* bytes) {
     const Call c(dtype, groups, per_group);
     if (c.status != ETP_OK) return c.status;
-    if (!bytes || K < 1 || N < 1 || K > ETP_LINEAR_MAX_CHANNELS || N > ETP_LINEAR_MAX_CHANNELS)
+    if (!bytes || K < 1 || N < 1 || K > ETP_LINEAR_MAX_CHANNELS || N > ETP_LINEAR_MAX_CHANNELS ||
+        (backward != 0 && backward != 1))
         return ETP_ERR_INVALID_ARG;
-    // the backward of the bias alone takes ranges of its own
-    const size_t all = etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N, true, true, true, true);
-    const size_t bias = etp::dense::linear_workspace_bytes(dtype == ETP_BF16, c.map.M, K, N, false, false, false, true);
-    *bytes = all > bias ? all : bias;
+    const bool bf16 = dtype == ETP_BF16, b = backward != 0;
+    *bytes = etp::dense::linear_workspace_bytes(bf16, c.map.M, K, N, !b, b, b, b);
+    // grad_bias alone takes ranges of its own
+    if (b) {
+        const size_t bias = etp::dense::linear_workspace_bytes(bf16, c.map.M, K, N, false, true, false, true);
+        if (bias > *bytes) *bytes = bias;
+    }
     return ETP_OK;
 }
 

@@ -519,6 +519,8 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
     };
     auto wait = [&](uint64_t* bar, unsigned parity) { return __all_sync(0xffffffffu, wait1(bar, parity)) != 0; };
     int images = 0;  // (first loader thread) image tiles asked for
+    if (P == Product::kGradW) launch_dependents();
+    if (IMAGE) wait_for_previous();  // for the image
 
     if (warp >= W::kEpi && warp < W::kMma) {  // loaders
         const int lt = t - 32 * W::kEpi, lw = lt >> 5;
@@ -867,6 +869,7 @@ __global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restri
     constexpr int R = Lay::kBMn ? Lay::kK : BN, C = Lay::kBMn ? BN : Lay::kK;  // W's rows and columns in a tile
     constexpr int kPerRow = C / 8, kUnits = R * kPerRow;
     const int ct = (cols + C - 1) / C, rt = (rows + R - 1) / R;
+    launch_dependents();
     const int u = blockIdx.x * 256 + threadIdx.x, tile = u / kUnits, w = u % kUnits;
     if (tile >= ct * rt) return;
     // tiles along the contraction are adjacent: it runs over W's rows (MN-major) or columns
@@ -882,29 +885,57 @@ __global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restri
 }
 
 // grad_W from the ranges' sums [splits][count] and grad_bias from [bias_rows][N], both in
-// order: 32 columns of up to 4 elements by 8 row lanes per block, then the 8 sums in order.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// a fixed order. A block: 128 elements of grad_W (V = 4 a thread, 16 row lanes) or 8 of
+// grad_bias (64 row lanes), then the row lanes' sums in order. Started while the sums are
+// still being written: waits for them itself.
+constexpr int kJoinThreads = 512;
+template <typename T, int V>
+__global__ void __launch_bounds__(kJoinThreads)
     etp_linear_join_kernel(const float* __restrict__ part, int splits, size_t count, T* __restrict__ gW,
                            const float* __restrict__ bias_part, int bias_rows, int N, T* __restrict__ gbias,
                            int blocks_w) {
-    __shared__ float red[8][32];
-    const int sub = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool is_bias = (int)blockIdx.x >= blocks_w;
-    const size_t cols = is_bias ? (size_t)N : count;
-    const size_t col = (size_t)(is_bias ? blockIdx.x - blocks_w : blockIdx.x) * 32 + lane;
-    const int rows = is_bias ? bias_rows : splits;
-    const float* src = is_bias ? bias_part : part;
-    float s = 0.f;
-    if (col < cols)
-#pragma unroll 8
-        for (int r = sub; r < rows; r += 8) s += src[(size_t)r * cols + col];
-    red[sub][lane] = s;
-    __syncthreads();
-    if (sub != 0 || col >= cols) return;
+    __shared__ float red[kJoinThreads * V];
+    wait_for_previous();
+    const int t = threadIdx.x;
+    if ((int)blockIdx.x < blocks_w) {
+        constexpr int kCols = 32, kRows = kJoinThreads / kCols;
+        const size_t col = ((size_t)blockIdx.x * kCols + t % kCols) * V;
+        const int sub = t / kCols;
+        float s[V];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
-    (is_bias ? gbias : gW)[col] = from_float<T>(s);
+        for (int j = 0; j < V; ++j) s[j] = 0.f;
+        if (col < count)
+#pragma unroll 4
+            for (int r = sub; r < splits; r += kRows) {
+                float v[V];
+                Pack<float, V>::load(part + (size_t)r * count + col, v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] += v[j];
+            }
+#pragma unroll
+        for (int j = 0; j < V; ++j) red[t * V + j] = s[j];
+        __syncthreads();
+        if (t >= kCols * V) return;
+        const size_t at = (size_t)blockIdx.x * kCols * V + t;
+        if (at >= count) return;
+        float sum = red[t];
+#pragma unroll
+        for (int w = 1; w < kRows; ++w) sum += red[w * kCols * V + t];
+        gW[at] = from_float<T>(sum);
+        return;
+    }
+    constexpr int kCols = 8, kRows = kJoinThreads / kCols;
+    const int col = ((int)blockIdx.x - blocks_w) * kCols + t % kCols, sub = t / kCols;
+    float s = 0.f;
+    if (col < N)
+#pragma unroll 8
+        for (int r = sub; r < bias_rows; r += kRows) s += bias_part[(size_t)r * N + col];
+    red[t] = s;
+    __syncthreads();
+    if (t >= kCols || col >= N) return;
+#pragma unroll 16
+    for (int w = 1; w < kRows; ++w) s += red[w * kCols + t];
+    gbias[col] = from_float<T>(s);
 }
 
 bool rows_aligned(const Rows& r, int elem, int bytes) {
@@ -934,7 +965,10 @@ cudaError_t launch_kernel(const Job& j, cudaStream_t s) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kBytes);
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
-    etp_linear_kernel<T, P, BN, VEC, IMAGE><<<j.items < sms ? j.items : sms, Warps<P>::kThreads, Lay::kBytes, s>>>(j);
+    const int grid = j.items < sms ? j.items : sms;
+    if (IMAGE)
+        return launch_after(etp_linear_kernel<T, P, BN, VEC, IMAGE>, grid, Warps<P>::kThreads, Lay::kBytes, s, j);
+    etp_linear_kernel<T, P, BN, VEC, IMAGE><<<grid, Warps<P>::kThreads, Lay::kBytes, s>>>(j);
     return cudaGetLastError();
 }
 
@@ -1075,12 +1109,13 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     const size_t count = a.gW && join ? (size_t)a.K * a.N : 0;
-    const int blocks_w = (int)((count + 31) / 32), blocks_b = a.gbias ? (a.N + 31) / 32 : 0;
+    const bool v4 = count % 4 == 0;
+    const int per = v4 ? 128 : 32;
+    const int blocks_w = (int)((count + per - 1) / per), blocks_b = a.gbias ? (a.N + 7) / 8 : 0;
     if (blocks_w + blocks_b == 0) return cudaSuccess;
-    etp_linear_join_kernel<T><<<blocks_w + blocks_b, 256, 0, s>>>(part, r.splits, count, static_cast<T*>(a.gW),
-                                                                  bias_part, r.splits * kBiasRows, a.N,
-                                                                  static_cast<T*>(a.gbias), blocks_w);
-    return cudaGetLastError();
+    return launch_after(v4 ? etp_linear_join_kernel<T, 4> : etp_linear_join_kernel<T, 1>, blocks_w + blocks_b,
+                        kJoinThreads, 0, s, part, r.splits, count, static_cast<T*>(a.gW), bias_part,
+                        r.splits * kBiasRows, a.N, static_cast<T*>(a.gbias), blocks_w);
 }
 
 }  // namespace

@@ -41,71 +41,98 @@ __device__ __forceinline__ float team_sum(float v, int team, float* red) {
     return v;
 }
 
+// One row's share of a lane: NV groups of V channels, zeros past C. Addresses are clamped
+// into the row and the loads unconditional: a branch around each would wait for each.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void load_row(const T* p, int C, int lane, int step, float (&v)[NV][V]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * step) * V;
+        Pack<T, V>::load(p + (c < C ? c : 0), v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((lane + i * step) * V >= C)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+}
+template <typename T, int V, int NV>
+__device__ __forceinline__ void load_param(const T* p, float none, int C, int lane, int step, float (&v)[NV][V]) {
+    if (p) {
+        load_row<T, V, NV>(p, C, lane, step, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] = none;
+    }
+}
+
+// Rows that a team has in flight at once.
+template <int V, int NV>
+constexpr int kRowsAtOnce = V * NV <= 4 ? 4 : V * NV <= 8 ? 2 : 1;
+
 template <typename T, int V, int NV, bool BLOCK>
 __global__ void __launch_bounds__(kThreads)
     etp_norm_fwd_kernel(RowMap map, int C, int team, float eps, Rows x, const T* __restrict__ weight,
                         const T* __restrict__ bias, Rows out, float* __restrict__ mean, float* __restrict__ rstd) {
     __shared__ float red[kWarps];
+    constexpr int U = kRowsAtOnce<V, NV>;
     const int step = BLOCK ? kThreads : team;
     const int lane = threadIdx.x & (step - 1);
     const int rows_per_block = kThreads / step;
     const int sub = threadIdx.x / step;
     float wv[NV][V], bv[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * step) * V;
-#pragma unroll
-        for (int j = 0; j < V; ++j) wv[i][j] = 1.f, bv[i][j] = 0.f;
-        if (c < C) {
-            if (weight) Pack<T, V>::load(weight + c, wv[i]);
-            if (bias) Pack<T, V>::load(bias + c, bv[i]);
-        }
-    }
+    load_param<T, V, NV>(weight, 1.f, C, lane, step, wv);
+    load_param<T, V, NV>(bias, 0.f, C, lane, step, bv);
+    const long long stride = (long long)gridDim.x * rows_per_block;
     // every lane of a warp runs the same number of steps: the sums are warp-collective
-    for (long long r0 = (long long)blockIdx.x * rows_per_block; r0 < map.M; r0 += (long long)gridDim.x * rows_per_block) {
-        const bool live = r0 + sub < map.M;
-        const int r = live ? (int)(r0 + sub) : 0;
-        const T* xs = static_cast<const T*>(x.p) + x.offset(map, r);
-        float v[NV][V];
-        float s = 0.f;
+    for (long long r0 = (long long)blockIdx.x * rows_per_block; r0 < map.M; r0 += U * stride) {
+        float v[U][NV][V];
+        int row[U];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * step) * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-            if (live && c < C) Pack<T, V>::load(xs + c, v[i]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) s += v[i][j];
+        for (int u = 0; u < U; ++u) {
+            const long long r = r0 + u * stride + sub;
+            row[u] = r < map.M ? (int)r : -1;
+            load_row<T, V, NV>(static_cast<const T*>(x.p) + x.offset(map, row[u] < 0 ? 0 : row[u]), C, lane, step, v[u]);
         }
-        const float mu = __fdiv_rn(team_sum<BLOCK>(s, team, red), (float)C);
-        // deviations from the rounded mean; what rounding took from it is their own mean
-        float q = 0.f, e = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if ((lane + i * step) * V < C)
+        for (int u = 0; u < U; ++u) {
+            float s = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    v[i][j] -= mu;
-                    e += v[i][j];
-                    q = fmaf(v[i][j], v[i][j], q);
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s += v[u][i][j];
+            const float mu = __fdiv_rn(team_sum<BLOCK>(s, team, red), (float)C);
+            // deviations from the rounded mean; what rounding took from it is their own mean
+            float q = 0.f, e = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if ((lane + i * step) * V < C)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        v[u][i][j] -= mu;
+                        e += v[u][i][j];
+                        q = fmaf(v[u][i][j], v[u][i][j], q);
+                    }
+            const float rest = __fdiv_rn(team_sum<BLOCK>(e, team, red), (float)C);
+            const float var = fmaxf(__fdiv_rn(team_sum<BLOCK>(q, team, red), (float)C) - rest * rest, 0.f);
+            const float rs = 1.f / sqrtf(var + eps);
+            if (row[u] < 0) continue;
+            T* os = static_cast<T*>(out.p) + out.offset(map, row[u]);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * step) * V;
+                if (c < C) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[u][i][j] = fmaf((v[u][i][j] - rest) * rs, wv[i][j], bv[i][j]);
+                    Pack<T, V>::store(os + c, v[u][i]);
                 }
-        const float rest = __fdiv_rn(team_sum<BLOCK>(e, team, red), (float)C);
-        const float var = fmaxf(__fdiv_rn(team_sum<BLOCK>(q, team, red), (float)C) - rest * rest, 0.f);
-        const float rs = 1.f / sqrtf(var + eps);
-        if (!live) continue;
-        T* os = static_cast<T*>(out.p) + out.offset(map, r);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * step) * V;
-            if (c < C) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] = fmaf((v[i][j] - rest) * rs, wv[i][j], bv[i][j]);
-                Pack<T, V>::store(os + c, v[i]);
             }
-        }
-        if (lane == 0) {
-            if (mean) mean[r] = mu + rest;
-            if (rstd) rstd[r] = rs;
+            if (lane == 0) {
+                if (mean) mean[row[u]] = mu + rest;
+                if (rstd) rstd[row[u]] = rs;
+            }
         }
     }
 }
@@ -118,63 +145,66 @@ __global__ void __launch_bounds__(kThreads)
                         float* __restrict__ part) {
     __shared__ float red[kWarps];
     extern __shared__ float acc[];  // [2][C], warp teams with PARAMS
+    constexpr int U = kRowsAtOnce<V, NV> > 2 ? 2 : kRowsAtOnce<V, NV>;
+    launch_dependents();
     const int step = BLOCK ? kThreads : team;
     const int lane = threadIdx.x & (step - 1);
     const int rows_per_block = kThreads / step;
     const int sub = threadIdx.x / step;
     float wv[NV][V], gws[NV][V], gbs[NV][V];
+    load_param<T, V, NV>(weight, 1.f, C, lane, step, wv);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * step) * V;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) wv[i][j] = 1.f, gws[i][j] = 0.f, gbs[i][j] = 0.f;
-        if (weight && c < C) Pack<T, V>::load(weight + c, wv[i]);
-    }
+        for (int j = 0; j < V; ++j) gws[i][j] = 0.f, gbs[i][j] = 0.f;
     const float inv = 1.f / (float)C;
-    for (long long r0 = (long long)blockIdx.x * rows_per_block; r0 < map.M; r0 += (long long)gridDim.x * rows_per_block) {
-        const bool live = r0 + sub < map.M;
-        const int r = live ? (int)(r0 + sub) : 0;
-        const T* xs = static_cast<const T*>(x.p) + x.offset(map, r);
-        const T* gs = static_cast<const T*>(g.p) + g.offset(map, r);
-        const float mu = live ? mean[r] : 0.f, rs = live ? rstd[r] : 0.f;
-        float xv[NV][V], gv[NV][V];
+    const long long stride = (long long)gridDim.x * rows_per_block;
+    for (long long r0 = (long long)blockIdx.x * rows_per_block; r0 < map.M; r0 += U * stride) {
+        float xv[U][NV][V], gv[U][NV][V], mu[U], rs[U];
+        int row[U];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * step) * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) xv[i][j] = mu, gv[i][j] = 0.f;
-            if (live && c < C) {
-                Pack<T, V>::load(xs + c, xv[i]);
-                Pack<T, V>::load(gs + c, gv[i]);
-            }
+        for (int u = 0; u < U; ++u) {
+            const long long r = r0 + u * stride + sub;
+            row[u] = r < map.M ? (int)r : -1;
+            const int at = row[u] < 0 ? 0 : row[u];
+            load_row<T, V, NV>(static_cast<const T*>(x.p) + x.offset(map, at), C, lane, step, xv[u]);
+            load_row<T, V, NV>(static_cast<const T*>(g.p) + g.offset(map, at), C, lane, step, gv[u]);
+            mu[u] = mean[at], rs[u] = rstd[at];
         }
-        float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int u = 0; u < U; ++u) {
+            float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float xh = (xv[i][j] - mu) * rs;
-                xv[i][j] = xh;
-                if (PARAMS) {
-                    gws[i][j] = fmaf(gv[i][j], xh, gws[i][j]);
-                    gbs[i][j] += gv[i][j];
+            for (int i = 0; i < NV; ++i) {
+                const bool on = row[u] >= 0 && (lane + i * step) * V < C;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (xv[u][i][j] - mu[u]) * rs[u];
+                    xv[u][i][j] = xh;
+                    if (PARAMS && on) {
+                        gws[i][j] = fmaf(gv[u][i][j], xh, gws[i][j]);
+                        gbs[i][j] += gv[u][i][j];
+                    }
+                    if (on) {
+                        gv[u][i][j] *= wv[i][j];
+                        s1 += gv[u][i][j];
+                        s2 = fmaf(gv[u][i][j], xh, s2);
+                    }
                 }
-                gv[i][j] *= wv[i][j];
-                s1 += gv[i][j];
-                s2 = fmaf(gv[i][j], xh, s2);
             }
-        if (!gx.p) continue;  // the same for every thread
-        s1 = team_sum<BLOCK>(s1, team, red) * inv;
-        s2 = team_sum<BLOCK>(s2, team, red) * inv;
-        if (!live) continue;
-        T* os = static_cast<T*>(gx.p) + gx.offset(map, r);
+            if (!gx.p) continue;  // the same for every thread
+            s1 = team_sum<BLOCK>(s1, team, red) * inv;
+            s2 = team_sum<BLOCK>(s2, team, red) * inv;
+            if (row[u] < 0) continue;
+            T* os = static_cast<T*>(gx.p) + gx.offset(map, row[u]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * step) * V;
-            if (c < C) {
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * step) * V;
+                if (c < C) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) gv[i][j] = rs * (gv[i][j] - s1 - xv[i][j] * s2);
-                Pack<T, V>::store(os + c, gv[i]);
+                    for (int j = 0; j < V; ++j) gv[u][i][j] = rs[u] * (gv[u][i][j] - s1 - xv[u][i][j] * s2);
+                    Pack<T, V>::store(os + c, gv[u][i]);
+                }
             }
         }
     }
@@ -216,22 +246,25 @@ __global__ void __launch_bounds__(kThreads)
     for (int c = threadIdx.x; c < 2 * C; c += kThreads) row[c] = acc[c];
 }
 
-// grad_w, grad_b (either may be null) from [n][2][C] partial rows, in row order: 32
-// columns by 8 row lanes per block, then the 8 sums in order.
+// grad_w, grad_b (either may be null) from [n][2][C] partial rows in a fixed order: 8
+// columns (a sector) by 64 row lanes per block, then the 64 sums in order. Started while
+// the partial rows are still being written: waits for them itself.
+constexpr int kJoinCols = 8, kJoinRows = 64;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinCols* kJoinRows)
     etp_norm_params_kernel(int n, int C, const float* __restrict__ part, T* __restrict__ gw, T* __restrict__ gb) {
-    __shared__ float red[kWarps][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), sub = threadIdx.x >> 5;
+    __shared__ float red[kJoinRows][kJoinCols + 1];
+    const int col = blockIdx.x * kJoinCols + threadIdx.x % kJoinCols, sub = threadIdx.x / kJoinCols;
+    wait_for_previous();
     float s = 0.f;
     if (col < 2 * C)
 #pragma unroll 8
-        for (int i = sub; i < n; i += kWarps) s += part[(size_t)i * 2 * C + col];
-    red[sub][threadIdx.x & 31] = s;
+        for (int i = sub; i < n; i += kJoinRows) s += part[(size_t)i * 2 * C + col];
+    red[sub][threadIdx.x % kJoinCols] = s;
     __syncthreads();
     if (sub != 0 || col >= 2 * C) return;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += red[w][threadIdx.x & 31];
+#pragma unroll 16
+    for (int w = 1; w < kJoinRows; ++w) s += red[w][threadIdx.x];
     T* o = col < C ? gw : gb;
     if (o) o[col < C ? col : col - C] = from_float<T>(s);
 }
@@ -302,7 +335,9 @@ cudaError_t pick(int C, A&&... a) {
             if (nv <= 8) return L<T, V, 8, false>::run(a...);
         }
         if constexpr (V == 1) {
+            if (nv <= 12) return L<T, V, 12, false>::run(a...);
             if (nv <= 16) return L<T, V, 16, false>::run(a...);
+            if (nv <= 20) return L<T, V, 20, false>::run(a...);
             return L<T, V, 32, false>::run(a...);
         }
         return cudaErrorInvalidValue;
@@ -359,14 +394,12 @@ cudaError_t norm_backward(bool bf16, bool v16, const RowMap& map, int C, const R
         if (e != cudaSuccess) return e;
     }
     if (!gweight && !gbias) return cudaSuccess;
-    const int blocks = (2 * C + 31) / 32;
+    const int blocks = (2 * C + kJoinCols - 1) / kJoinCols, threads = kJoinCols * kJoinRows;
     if (bf16)
-        etp_norm_params_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(
-            grid, C, part, static_cast<__nv_bfloat16*>(gweight), static_cast<__nv_bfloat16*>(gbias));
-    else
-        etp_norm_params_kernel<float><<<blocks, kThreads, 0, s>>>(grid, C, part, static_cast<float*>(gweight),
-                                                                  static_cast<float*>(gbias));
-    return cudaGetLastError();
+        return launch_after(etp_norm_params_kernel<__nv_bfloat16>, blocks, threads, 0, s, grid, C, part,
+                            static_cast<__nv_bfloat16*>(gweight), static_cast<__nv_bfloat16*>(gbias));
+    return launch_after(etp_norm_params_kernel<float>, blocks, threads, 0, s, grid, C, part,
+                        static_cast<float*>(gweight), static_cast<float*>(gbias));
 }
 
 }  // namespace dense

@@ -55,11 +55,12 @@ typedef enum { ETP_ACT_NONE = 0, ETP_ACT_SILU = 1 } etp_activation;
 #define ETP_LINEAR_MAX_CHANNELS 65536
 #define ETP_NORM_MAX_CHANNELS 8192
 
-/* Bytes of device workspace that etp_linear_forward and etp_linear_backward need at
- * most for these sizes (W rearranged for the tensor cores; partial sums of the weight
- * gradients over ranges of rows). 0 is possible. Host only; it reads the current
- * device's multiprocessor count. */
-ETP_API etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group, int K, int N,
+/* Bytes of device workspace that etp_linear_forward (backward = 0) or
+ * etp_linear_backward (backward = 1, whichever gradients are wanted) needs for these
+ * sizes: W rearranged for the tensor cores, partial sums of the weight gradients over
+ * ranges of rows. 0 is possible. Host only; it reads the current device's
+ * multiprocessor count. */
+ETP_API etp_status etp_linear_workspace_size(etp_dtype dtype, int groups, int per_group, int K, int N, int backward,
                                              size_t* bytes);
 
 /* Linear layer: z = x W + bias, out = act(z) + residual.

@@ -64,11 +64,13 @@ def test_linear_backward_refusals(lib):
     p = ctypes.c_void_p(PTR)
     size = ctypes.c_size_t()
     f = lib.etp_linear_workspace_size
-    assert f(0, 4, 2, 8, 8, ctypes.byref(size)) == OK and size.value > 0
-    assert f(0, 4, 2, 8, 8, None) == f(0, -1, 2, 8, 8, ctypes.byref(size)) == BAD
-    assert f(0, 4, 2, 0, 8, ctypes.byref(size)) == f(0, 4, 2, 8, 0, ctypes.byref(size)) == BAD
-    assert f(5, 4, 2, 8, 8, ctypes.byref(size)) == UNSUP
-    assert f(0, 1 << 20, 1 << 11, 8, 8, ctypes.byref(size)) == LARGE
+    assert f(0, 4, 2, 8, 8, 0, ctypes.byref(size)) == OK
+    assert f(0, 4, 2, 8, 8, 1, ctypes.byref(size)) == OK and size.value > 0
+    assert f(0, 4, 2, 8, 8, 1, None) == f(0, -1, 2, 8, 8, 1, ctypes.byref(size)) == BAD
+    assert f(0, 4, 2, 8, 8, 2, ctypes.byref(size)) == BAD
+    assert f(0, 4, 2, 0, 8, 0, ctypes.byref(size)) == f(0, 4, 2, 8, 0, 1, ctypes.byref(size)) == BAD
+    assert f(5, 4, 2, 8, 8, 0, ctypes.byref(size)) == UNSUP
+    assert f(0, 1 << 20, 1 << 11, 8, 8, 0, ctypes.byref(size)) == LARGE
 
     def call(dtype=0, groups=4, per=2, K=8, N=8, x=rows(), W=p, act=1, z=rows(), g=rows(), gx=rows(), gW=p, gb=p,
              ws=p, n=1 << 40):
