@@ -443,25 +443,31 @@ _DENSE_TYPES = {"torch.float32": ETP_F32, "torch.bfloat16": ETP_BF16}
 _ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "silu": ACT_SILU}
 
 
-def _dense_rows(t, name: str, like=None, channels=None):
-    """etp_rows of a tensor [M, C] or [groups, rows, C] whose channels are contiguous (None for None).
-    like: the tensor whose leading sizes and dtype it must share; channels: its C."""
+def _dense_lead(x, channels=None):
+    """(leading sizes, C) of x [M, C] or [groups, rows, C]; channels: the C it must have."""
+    shape = tuple(x.shape)
+    if len(shape) != 2 and len(shape) != 3:
+        raise ValueError(f"x: expected [rows, channels] or [groups, rows, channels], got {shape}")
+    if channels is not None and shape[-1] != channels:
+        raise ValueError(f"x: expected {channels} channels, got {shape[-1]}")
+    return shape[:-1], shape[-1]
+
+
+def _dense_rows(t, name: str, dtype, lead, C: int):
+    """etp_rows of a tensor of the given dtype and sizes (*lead, C) whose channels are contiguous (None for None)."""
     if t is None:
         return None
-    shape, st = t.shape, t.stride()
-    nd = len(shape)
-    if nd != 2 and nd != 3:
-        raise ValueError(f"{name}: expected [rows, channels] or [groups, rows, channels], got {tuple(shape)}")
-    if like is not None:
-        if t.dtype is not like.dtype:
-            raise ValueError(f"{name}: expected {like.dtype}, got {t.dtype}")
-        if shape[:-1] != like.shape[:-1]:
-            raise ValueError(f"{name}: expected leading sizes {tuple(like.shape[:-1])}, got {tuple(shape[:-1])}")
-    if channels is not None and shape[-1] != channels:
-        raise ValueError(f"{name}: expected {channels} channels, got {shape[-1]}")
-    if st[-1] != 1 and shape[-1] > 1:
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != (*lead, C) or (st[-1] != 1 and C > 1):
+        shape = tuple(t.shape)
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+        if shape[:-1] != lead:
+            raise ValueError(f"{name}: expected leading sizes {lead}, got {shape[:-1]}")
+        if shape[-1] != C:
+            raise ValueError(f"{name}: expected {C} channels, got {shape[-1]}")
         raise ValueError(f"{name}: channels must be contiguous (stride {st[-1]})")
-    return ctypes.byref(_Rows(t.data_ptr(), st[0], st[1] if nd == 3 else 0))
+    return ctypes.byref(_Rows(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0))
 
 
 def _dense_type(x):
@@ -471,12 +477,12 @@ def _dense_type(x):
     return code
 
 
-def _dense_vector(t, name: str, like, *shape):
-    """Address of a contiguous tensor of like's dtype and the given shape (None for None)."""
+def _dense_vector(t, name: str, dtype, *shape):
+    """Address of a contiguous tensor of the given dtype and shape (None for None)."""
     if t is None:
         return None
-    if t.dtype is not like.dtype or t.shape != shape:
-        raise ValueError(f"{name}: expected {like.dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
@@ -485,13 +491,11 @@ def _dense_vector(t, name: str, like, *shape):
 def _dense_device(x, *ts):
     """Index of the CUDA device of x, which the other tensors (None entries are skipped) must share."""
     index = x.get_device()
-    for t in (x, *ts):
-        if t is not None:
-            at = t.get_device()
-            if at < 0:
+    for t in ts:
+        if t is not None and t.get_device() != index or index < 0:
+            if index < 0 or t.get_device() < 0:
                 raise ValueError("tensors must be CUDA tensors: this library has no CPU path")
-            if at != index:
-                raise ValueError(f"tensors on different devices ({x.device}, {t.device})")
+            raise ValueError(f"tensors on different devices ({x.device}, {t.device})")
     return index
 
 
@@ -576,11 +580,6 @@ def _dense_outputs(outs, ins, in_place=()):
                 raise ValueError(f"{n} must not overlap {m}")
 
 
-def _dense_shape(x):
-    """(groups, per_group) of x's rows."""
-    return (x.shape[0], 1) if x.dim() == 2 else (x.shape[0], x.shape[1])
-
-
 def _check_linear(x, W, activation):
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation: expected 'none' or 'silu', got {activation!r}")
@@ -608,19 +607,20 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
     K, N = W.shape
-    xr = _dense_rows(x, "x", None, K)
-    Wp, bp = _dense_vector(W, "W", x, K, N), _dense_vector(bias, "bias", x, N)
-    rr = _dense_rows(residual, "residual", x, N)
+    dtype, (lead, _) = x.dtype, _dense_lead(x, K)
+    xr = _dense_rows(x, "x", dtype, lead, K)
+    Wp, bp = _dense_vector(W, "W", dtype, K, N), _dense_vector(bias, "bias", dtype, N)
+    rr = _dense_rows(residual, "residual", dtype, lead, N)
     if out is not None or z is not None:
         _dense_outputs([("out", out), ("z", z)], [("x", x), ("W", W), ("bias", bias), ("residual", residual)],
                        {("out", "residual")})
     if out is None:
-        out = x.new_empty((*x.shape[:-1], N))
+        out = x.new_empty((*lead, N))
     if z is None and save_z:
-        z = x.new_empty((*x.shape[:-1], N))
-    orow, zr = _dense_rows(out, "out", x, N), _dense_rows(z, "z", x, N)
+        z = x.new_empty((*lead, N))
+    orow, zr = _dense_rows(out, "out", dtype, lead, N), _dense_rows(z, "z", dtype, lead, N)
     index = _dense_device(x, W, bias, residual, z, out, workspace)
-    groups, per = _dense_shape(x)
+    groups, per = lead if len(lead) == 2 else (lead[0], 1)
     workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 0)
     _dense_call(index, "etp_linear_forward", _load().etp_linear_forward, code, groups, per, K, N, xr, Wp, bp, act, rr,
                 zr, orow, _ptr(workspace), nbytes, stream=stream)
@@ -634,12 +634,13 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
     K, N = W.shape
+    dtype, (lead, _) = x.dtype, _dense_lead(x, K)
     if act == ACT_NONE:
         z = None
     elif z is None:
         raise ValueError("z: the forward's pre-activation is needed for this activation")
-    xr, Wp = _dense_rows(x, "x", None, K), _dense_vector(W, "W", x, K, N)
-    gr, zr = _dense_rows(grad_out, "grad_out", x, N), _dense_rows(z, "z", x, N)
+    xr, Wp = _dense_rows(x, "x", dtype, lead, K), _dense_vector(W, "W", dtype, K, N)
+    gr, zr = _dense_rows(grad_out, "grad_out", dtype, lead, N), _dense_rows(z, "z", dtype, lead, N)
     if grad_x is not None or grad_W is not None or grad_bias is not None:
         _dense_outputs([("grad_x", grad_x), ("grad_W", grad_W), ("grad_bias", grad_bias)],
                        [("x", x), ("W", W), ("grad_out", grad_out), ("z", z)])
@@ -649,10 +650,10 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
         grad_W = x.new_empty((K, N))
     if "bias" in want and grad_bias is None:
         grad_bias = x.new_empty(N)
-    gxr = _dense_rows(grad_x, "grad_x", x, K)
-    gWp, gbp = _dense_vector(grad_W, "grad_W", x, K, N), _dense_vector(grad_bias, "grad_bias", x, N)
+    gxr = _dense_rows(grad_x, "grad_x", dtype, lead, K)
+    gWp, gbp = _dense_vector(grad_W, "grad_W", dtype, K, N), _dense_vector(grad_bias, "grad_bias", dtype, N)
     index = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
-    groups, per = _dense_shape(x)
+    groups, per = lead if len(lead) == 2 else (lead[0], 1)
     workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 1)
     _dense_call(index, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, xr, Wp, act, zr, gr,
                 gxr, gWp, gbp, _ptr(workspace), nbytes, stream=stream)
@@ -666,31 +667,25 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     import torch
 
     code = _dense_type(x)
-    xr = _dense_rows(x, "x")
-    lead, C = x.shape[:-1], x.shape[-1]
-    wp, bp = _dense_vector(weight, "weight", x, C), _dense_vector(bias, "bias", x, C)
+    dtype, (lead, C) = x.dtype, _dense_lead(x)
+    xr = _dense_rows(x, "x", dtype, lead, C)
+    wp, bp = _dense_vector(weight, "weight", dtype, C), _dense_vector(bias, "bias", dtype, C)
     if out is not None or mean is not None or rstd is not None:
         _dense_outputs([("out", out), ("mean", mean), ("rstd", rstd)], [("x", x), ("weight", weight), ("bias", bias)],
                        {("out", "x")})
     if out is None:
-        out = x.new_empty(x.shape)
+        out = x.new_empty((*lead, C))
     if mean is None:
         mean = x.new_empty(lead, dtype=torch.float32)
     if rstd is None:
         rstd = x.new_empty(lead, dtype=torch.float32)
-    orow = _dense_rows(out, "out", x, C)
-    _check_moments(x, mean, rstd)
+    orow = _dense_rows(out, "out", dtype, lead, C)
+    mp, rp = _dense_vector(mean, "mean", torch.float32, *lead), _dense_vector(rstd, "rstd", torch.float32, *lead)
     index = _dense_device(x, weight, bias, out, mean, rstd)
-    _dense_call(index, "etp_layer_norm_forward", _load().etp_layer_norm_forward, code, *_dense_shape(x), C, float(eps),
-                xr, wp, bp, orow, mean.data_ptr(), rstd.data_ptr(), stream=stream)
+    groups, per = lead if len(lead) == 2 else (lead[0], 1)
+    _dense_call(index, "etp_layer_norm_forward", _load().etp_layer_norm_forward, code, groups, per, C, float(eps), xr,
+                wp, bp, orow, mp, rp, stream=stream)
     return out, mean, rstd
-
-
-def _check_moments(x, mean, rstd):
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _expect(t, name, "float32", tuple(x.shape[:-1]))
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
 
 
 def layer_norm_workspace_size(M: int, C: int, dtype="float32", device=None) -> int:
@@ -707,12 +702,13 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
     """(grad_x, grad_weight, grad_bias) of layer_norm_forward for the cotangent grad_out (launches
     etp_layer_norm_backward); unwanted ones are None. weight: as in the forward (None: ones); mean, rstd: what it
     returned. grad_x may be grad_out or x itself."""
+    import torch
+
     code = _dense_type(x)
-    xr = _dense_rows(x, "x")
-    C = x.shape[-1]
-    gr = _dense_rows(grad_out, "grad_out", x, C)
-    wp = _dense_vector(weight, "weight", x, C)
-    _check_moments(x, mean, rstd)
+    dtype, (lead, C) = x.dtype, _dense_lead(x)
+    xr, gr = _dense_rows(x, "x", dtype, lead, C), _dense_rows(grad_out, "grad_out", dtype, lead, C)
+    wp = _dense_vector(weight, "weight", dtype, C)
+    mp, rp = _dense_vector(mean, "mean", torch.float32, *lead), _dense_vector(rstd, "rstd", torch.float32, *lead)
     if grad_x is not None or grad_weight is not None or grad_bias is not None:
         _dense_outputs([("grad_x", grad_x), ("grad_weight", grad_weight), ("grad_bias", grad_bias)],
                        [("x", x), ("weight", weight), ("mean", mean), ("rstd", rstd), ("grad_out", grad_out)],
@@ -723,16 +719,15 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
         grad_weight = x.new_empty(C)
     if "bias" in want and grad_bias is None:
         grad_bias = x.new_empty(C)
-    gxr = _dense_rows(grad_x, "grad_x", x, C)
-    gwp, gbp = _dense_vector(grad_weight, "grad_weight", x, C), _dense_vector(grad_bias, "grad_bias", x, C)
+    gxr = _dense_rows(grad_x, "grad_x", dtype, lead, C)
+    gwp, gbp = _dense_vector(grad_weight, "grad_weight", dtype, C), _dense_vector(grad_bias, "grad_bias", dtype, C)
     index = _dense_device(x, weight, mean, rstd, grad_out, grad_x, grad_weight, grad_bias, workspace)
-    groups, per = _dense_shape(x)
+    groups, per = lead if len(lead) == 2 else (lead[0], 1)
     nbytes = 0
     if grad_weight is not None or grad_bias is not None:
         workspace, nbytes = _dense_workspace(index, workspace, "etp_layer_norm_workspace_size", code, groups, per, C)
     _dense_call(index, "etp_layer_norm_backward", _load().etp_layer_norm_backward, code, groups, per, C, xr, wp,
-                mean.data_ptr(), rstd.data_ptr(), gr, gxr, gwp, gbp, _ptr(workspace) if nbytes else None, nbytes,
-                stream=stream)
+                mp, rp, gr, gxr, gwp, gbp, _ptr(workspace) if nbytes else None, nbytes, stream=stream)
     return grad_x, grad_weight, grad_bias
 
 

@@ -142,7 +142,7 @@ struct Layout {
     static constexpr int kFit = (int)((kSmemMost - kTail - kDepth * kRaw) / kSlot);
     static constexpr int kCap = kTmemSlots < (kRaw ? kWant + 1 : 6) ? kTmemSlots : (kRaw ? kWant + 1 : 6);
     static constexpr int kSlots = kFit < kCap ? kFit : kCap;
-    static constexpr int kLag = kTmemA && !kCopyB ? 0 : kRaw ? kDepth : kSlots - 1;
+    static constexpr int kLag = kTmemA && !kCopyB ? 0 : kRaw ? kDepth : kSlots / 2;  // the rest: ready for the MMAs
     static constexpr uint32_t kOffRaw = kSlots * kSlot;
     static constexpr uint32_t kOffBars = kOffRaw + kDepth * kRaw;
     static constexpr uint32_t kBytes = kOffBars + kTail;

@@ -6,8 +6,7 @@
 //
 // Bound by memory: each element is read once and written once. A row is held in the
 // registers of one team of lanes (a power of two up to a warp for up to 32 element
-// groups, then a warp with several groups per lane, a whole block above 1024
-// channels), so the second pass over it costs no further read. That pass takes the
+// groups, then a warp with several groups per lane, a whole block for wide rows), so the second pass over it costs no further read. That pass takes the
 // deviations d from the rounded mean and both sum(d) and sum(d^2): the first corrects
 // the mean for its own rounding, the variance is sum(d^2) / C minus that correction
 // squared, so a large common offset of a row costs no accuracy. Channel c always belongs to the
@@ -275,13 +274,19 @@ int pow2_at_least(int n) {
     return p;
 }
 
+// Channels above which a whole block takes a row. Single elements (V = 1) reach it sooner:
+// a warp would hold so many that few rows fit an SM (515 bf16 channels, 32768 rows,
+// backward: 116 us with a warp per row).
+__host__ __device__ constexpr int block_above(int V) { return V == 1 ? 256 : 1024; }
+
 // Teams and blocks of a launch: lanes per row, and as many blocks as keep the SMs full.
 struct Shape {
     int team, rows_per_block, grid;
 };
 Shape norm_shape(int M, int C, int V, int per_sm) {
     const int vecs = (C + V - 1) / V;
-    const bool block = C > 1024;
+    const bool block = C > block_above(V);
+    if (block && V == 1) per_sm = 8;
     Shape s;
     s.team = block ? kThreads : (vecs < 32 ? pow2_at_least(vecs) : 32);
     s.rows_per_block = kThreads / s.team;
@@ -326,7 +331,7 @@ struct BwdLaunch {
 template <template <typename, int, int, bool> class L, typename T, int V, typename... A>
 cudaError_t pick(int C, A&&... a) {
     const int vecs = (C + V - 1) / V;
-    if (C <= 1024) {
+    if (C <= block_above(V)) {
         const int nv = (vecs + 31) / 32;
         if (nv <= 1) return L<T, V, 1, false>::run(a...);
         if (nv <= 2) return L<T, V, 2, false>::run(a...);
@@ -334,24 +339,14 @@ cudaError_t pick(int C, A&&... a) {
         if constexpr (V <= 4) {
             if (nv <= 8) return L<T, V, 8, false>::run(a...);
         }
-        if constexpr (V == 1) {
-            if (nv <= 12) return L<T, V, 12, false>::run(a...);
-            if (nv <= 16) return L<T, V, 16, false>::run(a...);
-            if (nv <= 20) return L<T, V, 20, false>::run(a...);
-            return L<T, V, 32, false>::run(a...);
-        }
         return cudaErrorInvalidValue;
     }
     const int nv = (vecs + kThreads - 1) / kThreads;
     if constexpr (V == 8) {
         if (nv <= 1) return L<T, V, 1, true>::run(a...);
     }
-    if constexpr (V >= 4) {
-        if (nv <= 2) return L<T, V, 2, true>::run(a...);
-    }
-    if constexpr (V >= 4) {
-        if (nv <= 4) return L<T, V, 4, true>::run(a...);
-    }
+    if (nv <= 2) return L<T, V, 2, true>::run(a...);
+    if (nv <= 4) return L<T, V, 4, true>::run(a...);
     if constexpr (V <= 4) {
         if (nv <= 8) return L<T, V, 8, true>::run(a...);
     }
