@@ -595,7 +595,6 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                     tc::tmem_st8(col + p * (K / 2) + b * (kB / 2), w);
                 });
             }
-            tc::tmem_wait_st();
         };
         // -- B that is converted: units of 8 columns; a warp's 32 units of one index lie together in planes of their
         // first and their second 16 bytes (one plane of bfloat16). The lanes copy the warp's units together, so
@@ -668,6 +667,7 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
             advance(next);
         };
         auto arrive = [&](int slot) {  // this warp's part of the slot is written
+            if (Lay::kTmemA) tc::tmem_wait_st();
             tc::fence_proxy_async();
             if (Lay::kTmemA) tc::fence_before_sync();
             __syncwarp();
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
         }
     } else if (warp < W::kEpi) {
         constexpr int kCols = 4 * BN / W::kEpi, NR = kCols / 2;  // columns of a warp; registers of its 16 lanes
-        constexpr int kPiece = NR < 16 ? NR : 16;
+        constexpr int kPiece = NR < 16 ? NR : P == Product::kForward ? 16 : 8;  // of both halves at once, as registers allow
         const int quad = warp & 3, part = warp >> 2;
         const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
         int chunk = 0;
@@ -816,19 +816,22 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                 }
                 tc::fence_after_sync();
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int c = 0; c < NR; c += kPiece) {
+                    float v[2][kPiece];
 #pragma unroll
-                    for (int c = 0; c < NR; c += kPiece) {
-                        float v[kPiece];
-                        tc::tmem_ld_frag<kPiece>(base + ((uint32_t)(16 * h) << 16) + buf * BN + 2 * c, v);
-                        tc::tmem_wait_ld(v);
+                    for (int h = 0; h < 2; ++h)
+                        tc::tmem_ld_frag<kPiece>(base + ((uint32_t)(16 * h) << 16) + buf * BN + 2 * c, v[h]);
+                    tc::tmem_wait_ld(v[0]);
+                    tc::tmem_wait_ld(v[1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int j = 0; j < kPiece; j += 2) {
                             const float2 a = __fadd2_rn(make_float2(acc[h][c + j], acc[h][c + j + 1]),
-                                                        make_float2(v[j], v[j + 1]));
+                                                        make_float2(v[h][j], v[h][j + 1]));
                             acc[h][c + j] = a.x, acc[h][c + j + 1] = a.y;
                         }
-                    }
+                }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&tempty[buf]);
