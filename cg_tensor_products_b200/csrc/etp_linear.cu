@@ -27,8 +27,9 @@
 // a new accumulator, adds the small products first and the x0 w0 ones last (up to four
 // truncated additions of full size), and stages are added up in registers, rounded to
 // nearest. bfloat16 operands are one part (dz is rounded to it: the tensor core reads
-// nothing wider beside bf16 weights without a second product); their accumulator holds
-// 16 stages, whose truncations stay far below the result's own rounding.
+// nothing wider beside bf16 weights without a second product); their accumulator holds a
+// whole tile: up to 2^16 k in 4096 truncated additions, each 2^-24 of the sum on average,
+// stay below a sixteenth of the result's own rounding.
 //
 // grad_W contracts over the rows: the rows are cut into as many ranges as leave every
 // SM one, each range's sums go to the workspace, and a second launch adds them up in
@@ -45,17 +46,18 @@ enum class Product { kForward, kGradX, kGradW };
 constexpr int kRowsTile = 128;
 constexpr int kRangeK = 64;  // ranges of rows are whole multiples of it
 // Warps: the epilogue's (a quarter of the rows each, by a half or a quarter of the
-// columns), the loaders, one for the MMAs. The forward's epilogue has most to do and its
-// loaders least; the backward products have dz to compute in the loaders.
-template <Product P>
+// columns), the loaders, one for the MMAs. The float32 forward's epilogue has most to do
+// and its loaders least; the backward products have dz to compute in the loaders.
+template <typename T, Product P>
 struct Warps {
-    static constexpr int kEpi = P == Product::kForward ? 16 : 8;
-    static constexpr int kLoad = P == Product::kForward ? 4 : 8;
+    static constexpr int kEpi = P == Product::kForward && sizeof(T) == 4 ? 16 : 8;
+    static constexpr int kLoad = P == Product::kForward ? (sizeof(T) == 4 ? 4 : 8) : 16;
     static constexpr int kMma = kEpi + kLoad;
     static constexpr int kThreads = 32 * (kMma + 1);
     static constexpr int kLoaders = 32 * kLoad;
 };
-constexpr int kBiasRows = Warps<Product::kGradW>::kLoad;  // partial sums of dz per range: one per loader warp
+constexpr int kBiasRows = Warps<float, Product::kGradW>::kLoad;  // partial sums of dz per range: one per loader warp
+static_assert(kBiasRows == Warps<__nv_bfloat16, Product::kGradW>::kLoad, "loader warps of grad_W");
 constexpr int kWaitLimit = 1 << 22;
 constexpr int kRing = 2;  // accumulators in tensor memory
 constexpr uint32_t kSmemMost = 232448;
@@ -72,9 +74,10 @@ constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 // k of a stage. grad_W's float32 stages are half as long: they hold three operands.
 template <typename T, Product P>
 constexpr int kStageK = sizeof(T) == 4 && P == Product::kGradW ? 32 : 64;
-// Stages that one accumulator holds.
+// Stages that one accumulator holds: one of float32, a whole item's of bfloat16.
 template <typename T>
-constexpr int kChunk = sizeof(T) == 4 ? 1 : 16;
+constexpr int kChunk = sizeof(T) == 4 ? 1 : 1 << 20;
+constexpr int kMostRange = 1 << 16;  // rows of a range: bounds the truncations of a bfloat16 accumulator
 
 // Swizzled bf16 operand layouts in shared memory: rows of 128 bytes, the 16-byte chunk
 // index XORed with the row mod 8. MN-major: rows are k, 64 m (n) across; groups of 8 k
@@ -110,7 +113,7 @@ struct Share {
 // groups. IMAGE: B arrives as ready tiles.
 template <typename T, Product P, int BN, bool VEC, bool IMAGE>
 struct Layout {
-    using W = Warps<P>;
+    using W = Warps<T, P>;
     static constexpr int kK = kStageK<T, P>;
     static constexpr bool kAMn = P == Product::kGradW;  // A is MN-major (contraction over rows)
     static constexpr bool kBMn = P != Product::kGradX;  // B likewise
@@ -403,13 +406,13 @@ __device__ __forceinline__ unsigned long long row_offset(const Job& job, const R
     return V == Pairs::kFull ? (unsigned long long)(unsigned)m * r.gs : r.offset(job.map, m);
 }
 template <typename T, Product P, int COLS, Pairs V>
-__device__ __forceinline__ void finish(const Job& job, const Item& it, float (&acc)[2][COLS / 2], int quad, int part,
-                                       int lane) {
+__device__ __forceinline__ void finish(const Job& job, const Item& it, float (&acc)[2][COLS / 2],
+                                       int quad, int n0, int lane) {
     constexpr int kGroups = COLS / 8 < 4 ? COLS / 8 : 4;  // groups of 8 columns at a time
     const bool has_res = P == Product::kForward && job.residual.p != nullptr;
 #pragma unroll
     for (int g = 0; g < COLS / 8; g += kGroups) {
-        const int n = it.n0 + part * COLS + 8 * g + 2 * (lane & 3);
+        const int n = it.n0 + n0 + 8 * g + 2 * (lane & 3);
         float2 bias[kGroups];
         if constexpr (P == Product::kForward) {
 #pragma unroll
@@ -419,62 +422,52 @@ __device__ __forceinline__ void finish(const Job& job, const Item& it, float (&a
             }
         }
 #pragma unroll
-        for (int r0 = 0; r0 < 4; r0 += 2) {  // two rows at a time
-            float2 res[2][kGroups];
-            int left[2];
-            unsigned long long off[2];
+        for (int r = 0; r < 4; ++r) {  // a row at a time: two spill, which costs more than their overlap gives
+            const int m = it.m0 + quad * 32 + 8 * r + (lane >> 2);
+            const int left = V == Pairs::kFull || m < job.m ? job.n - n : 0;
+            float2 res[kGroups];
+            if (has_res) {
+                const T* p = static_cast<const T*>(job.residual.p) + row_offset<V>(job, job.residual, m) + n;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int m = it.m0 + quad * 32 + 8 * (r0 + q) + (lane >> 2);
-                left[q] = V == Pairs::kFull || m < job.m ? job.n - n : 0;
-                off[q] = n + (P == Product::kGradW ? (unsigned long long)m * job.n : row_offset<V>(job, job.out, m));
-                if (has_res) {
-                    const T* p = static_cast<const T*>(job.residual.p) + row_offset<V>(job, job.residual, m) + n;
-#pragma unroll
-                    for (int c = 0; c < kGroups; ++c) res[q][c] = load2<V>(p + 8 * c, left[q] - 8 * c);
-                }
+                for (int c = 0; c < kGroups; ++c) res[c] = load2<V>(p + 8 * c, left - 8 * c);
             }
+            float2 v[kGroups];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int r = r0 + q;
-                float2 v[kGroups];
+            for (int c = 0; c < kGroups; ++c)
+                v[c] = make_float2(acc[r >> 1][4 * (g + c) + 2 * (r & 1)], acc[r >> 1][4 * (g + c) + 2 * (r & 1) + 1]);
+            if constexpr (P == Product::kForward) {
 #pragma unroll
-                for (int c = 0; c < kGroups; ++c)
-                    v[c] = make_float2(acc[r >> 1][4 * (g + c) + 2 * (r & 1)], acc[r >> 1][4 * (g + c) + 2 * (r & 1) + 1]);
-                if constexpr (P == Product::kForward) {
+                for (int c = 0; c < kGroups; ++c) v[c].x += bias[c].x, v[c].y += bias[c].y;
+                if (job.z.p) {
+                    T* p = static_cast<T*>(job.z.p) + row_offset<V>(job, job.z, m) + n;
 #pragma unroll
-                    for (int c = 0; c < kGroups; ++c) v[c].x += bias[c].x, v[c].y += bias[c].y;
-                    if (job.z.p) {
-                        const int m = it.m0 + quad * 32 + 8 * r + (lane >> 2);
-                        T* p = static_cast<T*>(job.z.p) + row_offset<V>(job, job.z, m) + n;
-#pragma unroll
-                        for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left[q] - 8 * c);
-                    }
-                    if (job.silu)
-#pragma unroll
-                        for (int c = 0; c < kGroups; ++c) v[c].x = silu(v[c].x), v[c].y = silu(v[c].y);
-                    if (has_res)
-#pragma unroll
-                        for (int c = 0; c < kGroups; ++c) v[c].x += res[q][c].x, v[c].y += res[q][c].y;
+                    for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
                 }
-                if (P == Product::kGradW && job.part) {
-                    float* p = job.part + (size_t)it.split * job.m * job.n + off[q];
+                if (job.silu)
 #pragma unroll
-                    for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left[q] - 8 * c);
-                } else {
-                    T* p = (P == Product::kGradW ? static_cast<T*>(job.gW) : static_cast<T*>(job.out.p)) + off[q];
+                    for (int c = 0; c < kGroups; ++c) v[c].x = silu(v[c].x), v[c].y = silu(v[c].y);
+                if (has_res)
 #pragma unroll
-                    for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left[q] - 8 * c);
-                }
+                    for (int c = 0; c < kGroups; ++c) v[c].x += res[c].x, v[c].y += res[c].y;
+            }
+            if (P == Product::kGradW && job.part) {
+                float* p = job.part + ((size_t)it.split * job.m + m) * job.n + n;
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
+            } else {
+                T* p = P == Product::kGradW ? static_cast<T*>(job.gW) + (size_t)m * job.n + n
+                                            : static_cast<T*>(job.out.p) + row_offset<V>(job, job.out, m) + n;
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
             }
         }
     }
 }
 
 template <typename T, Product P, int BN, bool VEC, bool IMAGE>
-__global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const __grid_constant__ Job job) {
+__global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(const __grid_constant__ Job job) {
     using Lay = Layout<T, P, BN, VEC, IMAGE>;
-    using W = Warps<P>;
+    using W = Warps<T, P>;
     using ShareA = typename Lay::ShareA;
     using ShareB = typename Lay::ShareB;
     constexpr int NP = kParts<T>, K = Lay::kK, kSlots = Lay::kSlots;
@@ -513,6 +506,7 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
     const uint32_t tmem_a = tmem + kRing * BN;  // converted A: per slot, part after part
     // A bounded wait; false: leave the loops. wait(): the same answer for the whole warp.
     auto wait1 = [&](uint64_t* bar, unsigned parity) {
+        if (tc::mbar_wait(bar, parity, 1)) return true;  // mostly it is there
         const bool ok = !*abort_flag && tc::mbar_wait(bar, parity, kWaitLimit);
         if (!ok) *abort_flag = 1;
         return ok;
@@ -537,24 +531,24 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
         };
         int ring = 0;  // the stage's place among the kDepth in flight
         constexpr int kChunkElems = 16 / sizeof(T);
-        // -- A that is converted. A warp serves the 32 TMEM lanes that it may write (its index mod 4) and, with 8
-        // warps, one half of the k; it copies just what it reads, so that no other warp has to be waited for.
-        constexpr int kHalf = 4 * K / W::kLoad;          // k of a warp
-        constexpr int kRowBytes = Lay::kAMn ? 32 * (int)sizeof(T) : kHalf * (int)sizeof(T);  // of its block
-        constexpr int kRows = Lay::kAMn ? kHalf : 32, kRowChunks = kRowBytes / 16;
+        // -- A that is converted. A warp serves the 32 TMEM lanes that it may write (its index mod 4) and its share
+        // of the k; it copies just what it reads, so that no other warp has to be waited for.
+        constexpr int kShareK = 4 * K / W::kLoad;          // k of a warp
+        constexpr int kRowBytes = Lay::kAMn ? 32 * (int)sizeof(T) : kShareK * (int)sizeof(T);  // of its block
+        constexpr int kRows = Lay::kAMn ? kShareK : 32, kRowChunks = kRowBytes / 16;
         constexpr int kBlock = kRows * kRowBytes;
-        const int quad = warp & 3, khalf = lw >> 2;
+        const int quad = warp & 3, kshare = lw >> 2;
         auto block_a = [&](int z) {  // (z = 1: the pre-activation's)
             return smem + Lay::kOffRaw + ring * Lay::kRaw + z * Lay::kRawA + lw * kBlock;
         };
         auto chunk_a = [&](int r, int c) {  // chunk c of the block's row r: no two of 8 neighbouring rows in one bank
-            const int x = kRowChunks >= 8 ? r & 7 : kRowChunks == 4 ? (r >> 1) & 3 : 0;
+            const int x = kRowChunks >= 8 ? r & 7 : kRowChunks == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
             return (uint32_t)(r * kRowBytes + (((c & ~7) | ((c ^ x) & 7)) << 4));
         };
         auto fetch_a = [&](const Cursor& c, const Operand& o, int z) {
             constexpr int kPer = 32 / kRowChunks > 0 ? 32 / kRowChunks : 1;  // rows side by side in a warp's copies
             constexpr int kCols = kRowChunks < 32 ? kRowChunks : 32;
-            const int kk = c.it.k0 + c.ks * K + khalf * kHalf;
+            const int kk = c.it.k0 + c.ks * K + kshare * kShareK;
             const int row0 = Lay::kAMn ? kk : c.it.m0 + 32 * quad, col0 = Lay::kAMn ? c.it.m0 + 32 * quad : kk;
             const int rlim = Lay::kAMn ? c.it.k1 : o.nrows;
             unsigned char* blk = block_a(z);
@@ -563,11 +557,11 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                 [&](int i) { return blk + chunk_a(lane / kCols + kPer * i, lane % kCols); });
         };
         auto convert_a = [&](int slot) {
-            constexpr int kB = 16;  // k at a time
-            const uint32_t col = tmem_a + ((uint32_t)(quad * 32) << 16) + slot * Lay::kACols + khalf * (kHalf / 2);
+            constexpr int kB = kShareK < 16 ? kShareK : 16;  // k at a time
+            const uint32_t col = tmem_a + ((uint32_t)(quad * 32) << 16) + slot * Lay::kACols + kshare * (kShareK / 2);
             const unsigned char *blk = block_a(0), *zb = block_a(1);
 #pragma unroll
-            for (int b = 0; b < kHalf / kB; ++b) {
+            for (int b = 0; b < kShareK / kB; ++b) {
                 float v[kB];
                 if constexpr (Lay::kAMn) {
                     // (float32) the lane's column, k after k
@@ -592,7 +586,7 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
                     }
                 }
                 split_parts<T, kB>(v, [&](int p, const uint32_t(&w)[kB / 2]) {
-                    tc::tmem_st8(col + p * (K / 2) + b * (kB / 2), w);
+                    tc::tmem_st(col + p * (K / 2) + b * (kB / 2), w);
                 });
             }
         };
@@ -797,52 +791,77 @@ __global__ void __launch_bounds__(Warps<P>::kThreads, 1) etp_linear_kernel(const
             }
         }
     } else if (warp < W::kEpi) {
-        constexpr int kCols = 4 * BN / W::kEpi, NR = kCols / 2;  // columns of a warp; registers of its 16 lanes
-        constexpr int kPiece = NR < 16 ? NR : P == Product::kForward ? 16 : 8;  // of both halves at once, as registers allow
-        const int quad = warp & 3, part = warp >> 2;
-        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
+        constexpr int kCols = 4 * BN / W::kEpi;  // columns of a warp
+        const int quad = warp & 3, n0 = (warp >> 2) * kCols;
+        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + n0;
+        auto read = [&](int buf, int c, auto& v) {  // 16 lanes by NC columns from column c, both halves
+            constexpr int NC = sizeof(v) / (2 * sizeof(float)) * 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                tc::tmem_ld_frag<NC / 2>(base + ((uint32_t)(16 * h) << 16) + buf * BN + c, v[h]);
+            tc::tmem_wait_ld(v[0]);
+            tc::tmem_wait_ld(v[1]);
+        };
+        auto release = [&](int buf) {  // the accumulator has been read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&tempty[buf]);
+        };
+        auto end = [&](const Item& it, int at, auto cols_c, auto& acc) {
+            constexpr int NC = decltype(cols_c)::value;
+            if (job.vec_out && job.map.per.d == 1 && it.m0 + kRowsTile <= job.m && it.n0 + BN <= job.n)
+                finish<T, P, NC, Pairs::kFull>(job, it, acc, quad, n0 + at, lane);
+            else if (job.vec_out)
+                finish<T, P, NC, Pairs::kEven>(job, it, acc, quad, n0 + at, lane);
+            else
+                finish<T, P, NC, Pairs::kAny>(job, it, acc, quad, n0 + at, lane);
+        };
         int chunk = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
             const Item it = item_of<T, P>(job, i, BN);
-            float acc[2][NR];
-#pragma unroll
-            for (int j = 0; j < NR; ++j) acc[0][j] = acc[1][j] = 0.f;
-            for (int ks = 0; ks < it.stages; ks += kChunk<T>, ++chunk) {
+            if constexpr (sizeof(T) == 2) {  // one accumulator: pieces of it, read and finished in turn
+                constexpr int NC = kCols < 32 ? kCols : 32;
                 const int buf = chunk % kRing;
-                if (!wait(&tfull[buf], (chunk / kRing) & 1)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait(&tfull[buf], (chunk / kRing) & 1);
+                if (!ok) break;
                 tc::fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < NR; c += kPiece) {
-                    float v[2][kPiece];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        tc::tmem_ld_frag<kPiece>(base + ((uint32_t)(16 * h) << 16) + buf * BN + 2 * c, v[h]);
-                    tc::tmem_wait_ld(v[0]);
-                    tc::tmem_wait_ld(v[1]);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int j = 0; j < kPiece; j += 2) {
-                            const float2 a = __fadd2_rn(make_float2(acc[h][c + j], acc[h][c + j + 1]),
-                                                        make_float2(v[h][j], v[h][j + 1]));
-                            acc[h][c + j] = a.x, acc[h][c + j + 1] = a.y;
-                        }
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += NC) {
+                    float v[2][NC / 2];
+                    read(buf, c, v);
+                    if (c + NC == kCols) release(buf);
+                    end(it, c, Int<NC>{}, v);
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&tempty[buf]);
+                ++chunk;
+            } else {
+                constexpr int NR = kCols / 2, NP2 = NR < 16 ? NR : P == Product::kForward ? 16 : 8;
+                float acc[2][NR];
+#pragma unroll
+                for (int j = 0; j < NR; ++j) acc[0][j] = acc[1][j] = 0.f;
+                for (int ks = 0; ks < it.stages; ks += kChunk<T>, ++chunk) {
+                    const int buf = chunk % kRing;
+                    ok = wait(&tfull[buf], (chunk / kRing) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < NR; c += NP2) {  // as many columns at once as registers allow
+                        float v[2][NP2];
+                        read(buf, 2 * c, v);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = 0; j < NP2; j += 2) {
+                                const float2 a = __fadd2_rn(make_float2(acc[h][c + j], acc[h][c + j + 1]),
+                                                            make_float2(v[h][j], v[h][j + 1]));
+                                acc[h][c + j] = a.x, acc[h][c + j + 1] = a.y;
+                            }
+                    }
+                    release(buf);
+                }
+                if (!ok) break;
+                end(it, 0, Int<kCols>{}, acc);
             }
-            if (!ok) break;
-            if (job.vec_out && job.map.per.d == 1 && it.m0 + kRowsTile <= job.m && it.n0 + BN <= job.n)
-                finish<T, P, kCols, Pairs::kFull>(job, it, acc, quad, part, lane);
-            else if (job.vec_out)
-                finish<T, P, kCols, Pairs::kEven>(job, it, acc, quad, part, lane);
-            else
-                finish<T, P, kCols, Pairs::kAny>(job, it, acc, quad, part, lane);
         }
     }
     __syncthreads();
@@ -970,8 +989,8 @@ cudaError_t launch_kernel(const Job& j, cudaStream_t s) {
     const int sms = sm_count();
     const int grid = j.items < sms ? j.items : sms;
     if (IMAGE)
-        return launch_after(etp_linear_kernel<T, P, BN, VEC, IMAGE>, grid, Warps<P>::kThreads, Lay::kBytes, s, j);
-    etp_linear_kernel<T, P, BN, VEC, IMAGE><<<grid, Warps<P>::kThreads, Lay::kBytes, s>>>(j);
+        return launch_after(etp_linear_kernel<T, P, BN, VEC, IMAGE>, grid, Warps<T, P>::kThreads, Lay::kBytes, s, j);
+    etp_linear_kernel<T, P, BN, VEC, IMAGE><<<grid, Warps<T, P>::kThreads, Lay::kBytes, s>>>(j);
     return cudaGetLastError();
 }
 
@@ -1048,6 +1067,8 @@ Ranges ranges(int M, int K, int N) {
     int want = r.tiles < sms ? sms / r.tiles : 1;
     const int most = (stages + 3) / 4;
     want = want < most ? want : most;
+    const int least = (M + kMostRange - 1) / kMostRange;
+    want = want > least ? want : least;
     const int per = want > 0 ? (stages + want - 1) / want : 1;
     r.range = per * kRangeK;
     r.splits = stages > 0 ? (stages + per - 1) / per : 0;

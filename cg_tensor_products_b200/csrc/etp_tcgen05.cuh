@@ -172,9 +172,13 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[NC]) {
     for (int i = 0; i < NC; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// 8 consecutive 32-bit columns of this thread's TMEM lane (the warp's quarter of lanes,
-// thread = lane) from registers (warp-collective); complete after tmem_wait_st.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+// 4 or 8 consecutive 32-bit columns of this thread's TMEM lane (the warp's quarter of
+// lanes, thread = lane) from registers (warp-collective); complete after tmem_wait_st.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
 }
