@@ -51,15 +51,16 @@ constexpr int kRangeK = 64;  // ranges of rows are whole multiples of it
 template <typename T, Product P>
 struct Warps {
     static constexpr int kEpi = P == Product::kForward && sizeof(T) == 4 ? 16 : 8;
-    static constexpr int kLoad = P == Product::kForward ? (sizeof(T) == 4 ? 4 : 8) : 16;
+    static constexpr int kLoad = P == Product::kForward ? (sizeof(T) == 4 ? 4 : 8) : sizeof(T) == 4 ? 8 : 16;
     static constexpr int kMma = kEpi + kLoad;
     static constexpr int kThreads = 32 * (kMma + 1);
     static constexpr int kLoaders = 32 * kLoad;
 };
-constexpr int kBiasRows = Warps<float, Product::kGradW>::kLoad;  // partial sums of dz per range: one per loader warp
-static_assert(kBiasRows == Warps<__nv_bfloat16, Product::kGradW>::kLoad, "loader warps of grad_W");
+constexpr int kBiasRows = 16;  // most partial sums of dz per range: one per loader warp
 constexpr int kWaitLimit = 1 << 22;
-constexpr int kRing = 2;  // accumulators in tensor memory
+// Accumulators in tensor memory. One of 256 columns: the loaders' stages ahead cover its epilogue.
+template <int BN>
+constexpr int kRingOf = BN == 256 ? 1 : 2;
 constexpr uint32_t kSmemMost = 232448;
 
 __device__ int g_fault;
@@ -133,6 +134,7 @@ struct Layout {
     static constexpr uint32_t kRawB = kConvB ? ShareB::kIters * W::kLoaders * 8 * sizeof(T) : 0;
     static constexpr uint32_t kRawZ = kDzA ? kRawA : kDzB ? kRawB : 0;
     static constexpr uint32_t kRaw = kRawA + kRawZ + kRawB;
+    static constexpr int kRing = kRingOf<BN>;
     static constexpr uint32_t kTail = 256;  // barriers
     static constexpr int kWant = 3;         // slots, where there is room
     static constexpr int kTmemSlots = kACols ? (int)((512 - kRing * BN) / kACols) : 8;
@@ -175,7 +177,7 @@ struct Job {
     RowMap map;               // rows of the output operands
     Rows out, z, residual;
     const void* bias = nullptr;
-    int vec_out = 0;  // the epilogue's operands move 2 elements at a time
+    int vec_out = 0;  // the epilogue's operands move 1 (0), 2 (1) or 4 (2) elements at a time
     void* gW = nullptr;
     float *part = nullptr, *bias_part = nullptr;
     const unsigned char* image = nullptr;  // B as tiles of operand parts, or null
@@ -405,6 +407,21 @@ template <Pairs V>
 __device__ __forceinline__ unsigned long long row_offset(const Job& job, const Rows& r, int m) {
     return V == Pairs::kFull ? (unsigned long long)(unsigned)m * r.gs : r.offset(job.map, m);
 }
+// bfloat16 pairs of a row's groups c, c + 1 (16 columns, one sector): traded between the
+// row's 4 lanes so that each stores 4 neighbouring columns and the sector is written whole
+// (grad_x: 131072 x 256 bf16 67 -> 61 us; the forward's longer epilogue loses by it, 112 -> 171 us
+// at 166517 x 512).
+template <int G>
+__device__ __forceinline__ void store_quads(__nv_bfloat16* row, const float2 (&v)[G], int lane) {
+    const int q = lane & 3, src = (lane & ~3) + 2 * (q & 1);
+#pragma unroll
+    for (int c = 0; c < G; c += 2) {
+        const uint32_t a = pack_bf16(v[c].x, v[c].y), b = pack_bf16(v[c + 1].x, v[c + 1].y);
+        const uint32_t a0 = __shfl_sync(0xffffffffu, a, src), b0 = __shfl_sync(0xffffffffu, b, src);
+        const uint32_t a1 = __shfl_sync(0xffffffffu, a, src + 1), b1 = __shfl_sync(0xffffffffu, b, src + 1);
+        *reinterpret_cast<uint2*>(row + 8 * c + 4 * q) = make_uint2(q < 2 ? a0 : b0, q < 2 ? a1 : b1);
+    }
+}
 template <typename T, Product P, int COLS, Pairs V>
 __device__ __forceinline__ void finish(const Job& job, const Item& it, float (&acc)[2][COLS / 2],
                                        int quad, int n0, int lane) {
@@ -450,7 +467,10 @@ __device__ __forceinline__ void finish(const Job& job, const Item& it, float (&a
 #pragma unroll
                     for (int c = 0; c < kGroups; ++c) v[c].x += res[c].x, v[c].y += res[c].y;
             }
-            if (P == Product::kGradW && job.part) {
+            if constexpr (sizeof(T) == 2 && V == Pairs::kFull && P == Product::kGradX && kGroups % 2 == 0) {
+                store_quads<kGroups>(static_cast<T*>(job.out.p) + row_offset<V>(job, job.out, m) + n - 2 * (lane & 3), v,
+                                     lane);
+            } else if (P == Product::kGradW && job.part) {
                 float* p = job.part + ((size_t)it.split * job.m + m) * job.n + n;
 #pragma unroll
                 for (int c = 0; c < kGroups; ++c) store2<V>(p + 8 * c, v[c], left - 8 * c);
@@ -470,7 +490,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
     using W = Warps<T, P>;
     using ShareA = typename Lay::ShareA;
     using ShareB = typename Lay::ShareB;
-    constexpr int NP = kParts<T>, K = Lay::kK, kSlots = Lay::kSlots;
+    constexpr int NP = kParts<T>, K = Lay::kK, kSlots = Lay::kSlots, kRing = Lay::kRing;
     constexpr bool kDzA = Lay::kDzA, kDzB = Lay::kDzB;
 
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -807,9 +827,10 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&tempty[buf]);
         };
+        constexpr int kFullVec = sizeof(T) == 2 && P == Product::kGradX ? 2 : 1;
         auto end = [&](const Item& it, int at, auto cols_c, auto& acc) {
             constexpr int NC = decltype(cols_c)::value;
-            if (job.vec_out && job.map.per.d == 1 && it.m0 + kRowsTile <= job.m && it.n0 + BN <= job.n)
+            if (job.vec_out >= kFullVec && job.map.per.d == 1 && it.m0 + kRowsTile <= job.m && it.n0 + BN <= job.n)
                 finish<T, P, NC, Pairs::kFull>(job, it, acc, quad, n0 + at, lane);
             else if (job.vec_out)
                 finish<T, P, NC, Pairs::kEven>(job, it, acc, quad, n0 + at, lane);
@@ -1018,7 +1039,9 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
 }
 
 // How the forward and grad_x products of M rows, k contracted and n output columns are
-// tiled: the widest tile that still gives every SM one, or the narrowest; and whether W
+// tiled: the widest tile that still gives every SM one, or the narrowest (256 columns
+// with bfloat16 alone: A is then read, and dz formed, half as often; 131072 x 256 -> 256
+// grad_x 102 us with 128, 61 us with 256; float32 parts leave no tensor memory for it); and whether W
 // is converted ahead (an image), which pays once a CTA would convert it more than once.
 struct Tiling {
     int bn;
@@ -1029,7 +1052,7 @@ Tiling tiling(bool bf16, Product p, int M, int k, int n) {
     const long long mt = ((long long)M + kRowsTile - 1) / kRowsTile;
     const int sms = sm_count();
     Tiling t;
-    t.bn = n > 64 && mt * ((n + 127) / 128) >= sms ? 128 : n > 32 && mt * ((n + 63) / 64) >= sms ? 64 : 32;
+    t.bn = bf16 && p == Product::kGradX && n > 128 && mt * ((n + 255) / 256) >= sms ? 256 : n > 64 && mt * ((n + 127) / 128) >= sms ? 128 : n > 32 && mt * ((n + 63) / 64) >= sms ? 64 : 32;
     t.image = mt * ((n + t.bn - 1) / t.bn) >= 2 * sms;
     constexpr int K = 64;  // k of a stage of either
     static_assert(kStageK<float, Product::kForward> == K && kStageK<float, Product::kGradX> == K, "image tiles");
@@ -1047,6 +1070,9 @@ cudaError_t launch(Job& j, int bn, int splits, unsigned char* image, cudaStream_
     j.tiles = FastDiv((int)tiles);
     j.items = (int)tiles * splits;
     switch (bn) {
+        case 256:
+            if constexpr (sizeof(T) == 2 && P == Product::kGradX) return launch_bn<T, P, 256>(j, image, s);
+            return cudaErrorInvalidValue;
         case 128: return launch_bn<T, P, 128>(j, image, s);
         case 64: return launch_bn<T, P, 64>(j, image, s);
         default: return launch_bn<T, P, 32>(j, image, s);
@@ -1104,7 +1130,8 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
         j.m = a.map.M, j.n = a.K, j.k = a.N;
         j.map = a.map;
         j.out = a.gx;
-        j.vec_out = a.K % 2 == 0 && rows_aligned(a.gx, elem, 2 * elem);
+        for (int v = 2; v <= 4; v *= 2)
+            if (a.K % v == 0 && rows_aligned(a.gx, elem, v * elem)) j.vec_out = v / 2;
         const Tiling t = tiling(elem == 2, Product::kGradX, j.m, j.k, j.n);
         const cudaError_t e = launch<T, Product::kGradX>(
             j, t.bn, 1, t.image ? reinterpret_cast<unsigned char*>(a.ws) : nullptr, s);
@@ -1139,7 +1166,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
     if (blocks_w + blocks_b == 0) return cudaSuccess;
     return launch_after(v4 ? etp_linear_join_kernel<T, 4> : etp_linear_join_kernel<T, 1>, blocks_w + blocks_b,
                         kJoinThreads, 0, s, part, r.splits, count, static_cast<T*>(a.gW), bias_part,
-                        r.splits * kBiasRows, a.N, static_cast<T*>(a.gbias), blocks_w);
+                        r.splits * Warps<T, Product::kGradW>::kLoad, a.N, static_cast<T*>(a.gbias), blocks_w);
 }
 
 }  // namespace
