@@ -1,6 +1,8 @@
 """Host-side checks of the dense row operators (no GPU): every declared symbol is exported, and the C ABI and
 the binding refuse bad arguments before any launch. Every call that passes pointers is built to fail a check."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -17,6 +19,30 @@ PTR = 0x10000  # never dereferenced
 def lib():
     etp_build.build()
     return etp._load()
+
+
+def test_header_is_plain_c(tmp_path):
+    """etp_dense.h compiles as C and its calls link and refuse bad arguments from a C program."""
+    src = tmp_path / "dense.c"
+    src.write_text("""
+#include <etp_dense.h>
+int main(void) {
+    etp_rows x = {0, 128, 0};
+    size_t n = 0;
+    if (etp_linear_workspace_size(ETP_F32, 1000, 1, 64, 64, 1, &n) != ETP_OK || n == 0) return 1;
+    if (etp_layer_norm_workspace_size(ETP_BF16, 1000, 3, 64, &n) != ETP_OK || n == 0) return 2;
+    if (etp_linear_forward(ETP_F32, 4, 1, 64, 64, &x, 0, 0, ETP_ACT_SILU, 0, 0, &x, 0, 0, 0) != ETP_ERR_INVALID_ARG) return 3;
+    if (etp_linear_backward(ETP_F32, 4, 1, 64, 64, &x, 0, ETP_ACT_NONE, 0, &x, 0, 0, 0, 0, 0, 0) != ETP_OK) return 4;
+    if (etp_layer_norm_forward(ETP_F32, 4, 1, 64, 1e-5f, &x, 0, 0, &x, 0, 0, 0) != ETP_ERR_INVALID_ARG) return 5;
+    if (etp_layer_norm_backward(ETP_F32, 4, 1, 64, &x, 0, 0, 0, &x, &x, 0, 0, 0, 0, 0) != ETP_ERR_INVALID_ARG) return 6;
+    return 0;
+}
+""")
+    etp_build.build()
+    libdir, exe = os.path.dirname(etp.LIB_PATH), str(tmp_path / "dense")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.dirname(etp.DENSE_HEADER_PATH), str(src), "-L",
+                    libdir, "-letp", f"-Wl,-rpath,{libdir}", "-o", exe], check=True, capture_output=True, text=True)
+    assert subprocess.run([exe], timeout=60).returncode == 0
 
 
 def rows(data=PTR, gs=64, rs=8):

@@ -2,8 +2,9 @@
 
 Tolerances, per element, with S the sum of the absolute values that the element adds up:
   - float32 products: each operand is split exactly, products dropped or rounded are below 2^-22, and at most
-    four truncated (2^-23) and one rounded (2^-24) addition per 64 terms touch a partial sum, so the error is below
+    four truncated (2^-23) and two rounded (2^-24) additions per 64 terms touch a partial sum, so the error is below
     (8 + T / 8) 2^-23 S for T terms; as a vector (2-norm) the errors of T random terms stay below 2^-20;
+  - bfloat16 products: T / 16 truncated additions (2^-23) in one accumulator, within the same bound;
   - the activation: exp within 4 ulp of its own size and a handful of roundings, 2^-20 (1 + |z|);
   - dz = grad_out act'(z) of bfloat16 operands enters the products rounded to bfloat16, 2^-8 of each dz (not the
     bias gradient, and not without an activation, where dz is grad_out itself);
@@ -143,11 +144,11 @@ def test_linear_strides_and_broadcasts(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_linear_many_rows(dtype):
+@pytest.mark.parametrize("M,K,N", [(70001, 64, 96), (38001, 200, 264), (40000, 256, 256), (38017, 131, 257)])
+def test_linear_many_rows(M, K, N, dtype):
     """More rows than one pass of the GPU takes, with the weight gradients summed over all of them."""
-    normal = _rand(9)
-    M, K, N = 70001, 64, 96
-    x, W = normal(M, K, dtype=dtype), normal(K, N, dtype=dtype, scale=0.125)
+    normal = _rand(9 + K)
+    x, W = normal(M, K, dtype=dtype), normal(K, N, dtype=dtype, scale=K**-0.5)
     _check_linear(x, W, normal(N, dtype=dtype), "silu", normal(M, N, dtype=dtype), normal(M, N, dtype=dtype))
 
 
@@ -306,6 +307,29 @@ def test_streams_and_captured_graphs():
         ref = want if i == 0 else block(g, x)
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(outs[i], ref))
+
+
+def test_two_calls_at_once():
+    """Calls on two streams that overlap on the GPU, each with its own workspace."""
+    normal = _rand(12)
+    x, W, g = normal(50000, 96), normal(96, 160, scale=0.1), normal(50000, 160)
+    want = (etp.linear_forward(x, W), *etp.linear_backward(x, W, g), *etp.layer_norm_forward(x))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append((etp.linear_forward(x, W), *etp.linear_backward(x, W, g), *etp.layer_norm_forward(x)))
+    torch.cuda.synchronize()
+    for outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    ws = torch.empty(etp.linear_workspace_size(50000, 96, 160, backward=True), dtype=torch.uint8, device="cuda")
+    mine = etp.linear_backward(x, W, g, workspace=ws, stream=streams[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(mine, want[1:4]))
+    with pytest.raises(etp.EtpError, match="workspace"):
+        etp.linear_backward(x, W, g, workspace=ws[:16])
+    assert etp.device_fault() == 0
 
 
 def test_update_block_with_the_edge_tensor_product():
