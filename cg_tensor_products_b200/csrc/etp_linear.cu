@@ -537,6 +537,15 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
     };
     auto wait = [&](uint64_t* bar, unsigned parity) { return __all_sync(0xffffffffu, wait1(bar, parity)) != 0; };
     int images = 0;  // (first loader thread) image tiles asked for
+    // Where a whole contraction is one stage, its converted A serves all column tiles of a row block: the A
+    // columns in tensor memory then change with the row block, not with the stage (16384 x 64 -> 4352: 95 us
+    // without, 80 us with).
+    const bool keep_a = Lay::kTmemA && !Lay::kConvB && !Lay::kCopyB && job.k <= K;
+    // This CTA's items lo, lo + step, .. below hi: one after another then, else taken in turn with the other CTAs,
+    // so that those that run together share a row block in L2.
+    const int step = keep_a ? 1 : gridDim.x;
+    const int lo = keep_a ? (int)((long long)job.items * blockIdx.x / gridDim.x) : blockIdx.x;
+    const int hi = keep_a ? (int)((long long)job.items * (blockIdx.x + 1) / gridDim.x) : job.items;
     if (P == Product::kGradW) launch_dependents();
     if (IMAGE) wait_for_previous();  // for the image
 
@@ -546,12 +555,12 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
         struct Cursor {
             int i, ks;
             Item it;
-        } now{(int)blockIdx.x, 0, item_of<T, P, MT>(job, blockIdx.x, BN)}, next = now;
+        } now{lo, 0, item_of<T, P, MT>(job, lo, BN)}, next = now;
         auto advance = [&](Cursor& c) {
             if (++c.ks < c.it.stages) return;
             c.ks = 0;
-            c.i += gridDim.x;
-            if (c.i < job.items) c.it = item_of<T, P, MT>(job, c.i, BN);
+            c.i += step;
+            if (c.i < hi) c.it = item_of<T, P, MT>(job, c.i, BN);
         };
         int ring = 0;  // the stage's place among the kDepth in flight
         constexpr int kChunkElems = 16 / sizeof(T);
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
                                                                          [&](int i) { return dst + S::offset(lt, i); });
         };
         auto fetch = [&]() {  // the fetch cursor's stage, one group of copies
-            if (next.i < job.items) {
+            if (next.i < hi) {
                 if constexpr (Lay::kTmemA) {
                     fetch_a(next, job.A, 0);
                     if constexpr (kDzA) {
@@ -682,6 +691,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
                 }
             }
             copy_commit();
+            if (Lay::kTmemA && keep_a) next.i += job.ntn.d - 1 - (next.i - (next.it.m0 / kRowsTile) * job.ntn.d);
             advance(next);
         };
         auto arrive = [&](int slot) {  // this warp's part of the slot is written
@@ -696,7 +706,8 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
             for (ring = 0; ring < Lay::kDepth; ++ring) fetch();
             ring = 0;
         }
-        for (; now.i < job.items; ++n) {
+        int blocks = 0;  // row blocks converted (keep_a)
+        for (; now.i < hi; ++n) {
             const int slot = n % kSlots;
             if (n >= kSlots && !wait(&empty[slot], (n / kSlots - 1) & 1)) break;
             if (Lay::kTmemA) tc::fence_after_sync();
@@ -718,18 +729,22 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
                 copy_tile(ShareB{}, job.B, sb, Lay::kBMn ? kk : now.it.n0, job.B.nrows, Lay::kBMn ? now.it.n0 : kk);
             }
             if constexpr (Lay::kRaw > 0) {
-                copy_wait<Lay::kDepth - 1>();
-                __syncwarp();
-                if constexpr (Lay::kTmemA) convert_a(slot);
-                if constexpr (Lay::kConvB) {
-                    if (kDzB && now.ks == 0)
+                const bool fresh = !(Lay::kTmemA && keep_a) || now.i == lo || now.it.n0 == 0;
+                if (fresh) {
+                    copy_wait<Lay::kDepth - 1>();
+                    __syncwarp();
+                    if constexpr (Lay::kTmemA) convert_a(keep_a ? blocks % kSlots : slot);
+                    if constexpr (Lay::kConvB) {
+                        if (kDzB && now.ks == 0)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) bsum[j] = 0.f;
-                    convert_b(sb);
+                            for (int j = 0; j < 8; ++j) bsum[j] = 0.f;
+                        convert_b(sb);
+                    }
+                    __syncwarp();  // read by all lanes
+                    fetch();       // its group takes in the copies into the slot
+                    ring = ring + 1 == Lay::kDepth ? 0 : ring + 1;
+                    ++blocks;
                 }
-                __syncwarp();  // read by all lanes
-                fetch();       // its group takes in the copies into the slot
-                ring = ring + 1 == Lay::kDepth ? 0 : ring + 1;
             } else {
                 copy_commit();
             }
@@ -767,11 +782,11 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
         if constexpr (!Lay::kTmemA) base_a = operand_desc<Lay::kAMn, K>(tc::smem_u32(smem + NP * Lay::kBPart));
         const uint64_t base_b = operand_desc<Lay::kBMn, K>(tc::smem_u32(smem));
         // the stage's MMAs, unrolled: operand addresses are the slot's plus constants
-        auto issue = [&](auto steps_c, uint32_t d, int slot, bool first) {
+        auto issue = [&](auto steps_c, uint32_t d, int slot, int aslot, bool first) {
             constexpr int S = decltype(steps_c)::value;
             const uint64_t db = base_b + (uint64_t)(slot * (Lay::kSlot >> 4));
             [[maybe_unused]] const uint64_t da = base_a + (uint64_t)(slot * (Lay::kSlot >> 4));
-            [[maybe_unused]] const uint32_t ta = tmem_a + slot * Lay::kACols;
+            [[maybe_unused]] const uint32_t ta = tmem_a + aslot * Lay::kACols;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -788,8 +803,10 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
         };
         int n = 0, chunk = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
+        int block = -1;
+        for (int i = lo; i < hi && ok; i += step) {
             const Item it = item_of<T, P, MT>(job, i, BN);
+            if (i == lo || it.n0 == 0) ++block;
             for (int ks = 0; ks < it.stages; ++ks, ++n) {
                 const int slot = n % kSlots, buf = chunk % kRing;
                 const bool first = ks % kChunk<T> == 0;
@@ -801,14 +818,15 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
                 tc::fence_after_sync();
                 const int left = it.k1 - it.k0 - ks * K;
                 const uint32_t d = tmem + buf * Lay::kAcc;
+                const int aslot = keep_a ? block % kSlots : slot;
                 if (left > K - 16)
-                    issue(Int<K / 16>{}, d, slot, first);
+                    issue(Int<K / 16>{}, d, slot, aslot, first);
                 else if (K == 64 && left > 32)
-                    issue(Int<K == 64 ? 3 : 1>{}, d, slot, first);
+                    issue(Int<K == 64 ? 3 : 1>{}, d, slot, aslot, first);
                 else if (K == 64 && left > 16)
-                    issue(Int<K == 64 ? 2 : 1>{}, d, slot, first);
+                    issue(Int<K == 64 ? 2 : 1>{}, d, slot, aslot, first);
                 else
-                    issue(Int<1>{}, d, slot, first);
+                    issue(Int<1>{}, d, slot, aslot, first);
                 tc::mma_commit(&empty[slot]);
                 if (ks + 1 == it.stages || (ks + 1) % kChunk<T> == 0) {
                     tc::mma_commit(&tfull[buf]);
@@ -845,7 +863,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
         };
         int chunk = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < job.items && ok; i += gridDim.x) {
+        for (int i = lo; i < hi && ok; i += step) {
             const Item it = item_of<T, P, MT>(job, i, BN);
             if constexpr (sizeof(T) == 2) {  // one accumulator: pieces of it, read and finished in turn
                 constexpr int NC = kCols < 32 ? kCols : 32;

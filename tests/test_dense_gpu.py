@@ -144,7 +144,7 @@ def test_linear_strides_and_broadcasts(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("M,K,N", [(70001, 64, 96), (38001, 200, 264), (40000, 256, 256), (38017, 131, 257)])
+@pytest.mark.parametrize("M,K,N", [(70001, 64, 96), (30001, 48, 600), (38001, 200, 264), (40000, 256, 256), (38017, 131, 257)])
 def test_linear_many_rows(M, K, N, dtype):
     """More rows than one pass of the GPU takes, with the weight gradients summed over all of them."""
     normal = _rand(9 + K)
