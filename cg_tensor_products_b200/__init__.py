@@ -470,6 +470,14 @@ def _dense_rows(t, name: str, dtype, lead, C: int):
     return ctypes.byref(_Rows(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0))
 
 
+def _dense_new(x, lead, C: int):
+    """(a new contiguous tensor of sizes (*lead, C) like x, its etp_rows)."""
+    import torch
+
+    t = torch.empty_like(x) if x.shape[-1] == C and x.is_contiguous() else x.new_empty((*lead, C))
+    return t, ctypes.byref(_Rows(t.data_ptr(), C if len(lead) == 1 else lead[1] * C, C))
+
+
 def _dense_type(x):
     code = _DENSE_TYPES.get(str(x.dtype))
     if code is None:
@@ -614,11 +622,8 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     if out is not None or z is not None:
         _dense_outputs([("out", out), ("z", z)], [("x", x), ("W", W), ("bias", bias), ("residual", residual)],
                        {("out", "residual")})
-    if out is None:
-        out = x.new_empty((*lead, N))
-    if z is None and save_z:
-        z = x.new_empty((*lead, N))
-    orow, zr = _dense_rows(out, "out", dtype, lead, N), _dense_rows(z, "z", dtype, lead, N)
+    out, orow = (out, _dense_rows(out, "out", dtype, lead, N)) if out is not None else _dense_new(x, lead, N)
+    z, zr = (z, _dense_rows(z, "z", dtype, lead, N)) if z is not None or not save_z else _dense_new(x, lead, N)
     index = _dense_device(x, W, bias, residual, z, out, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
     workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 0)
@@ -644,13 +649,13 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
     if grad_x is not None or grad_W is not None or grad_bias is not None:
         _dense_outputs([("grad_x", grad_x), ("grad_W", grad_W), ("grad_bias", grad_bias)],
                        [("x", x), ("W", W), ("grad_out", grad_out), ("z", z)])
+    gxr = _dense_rows(grad_x, "grad_x", dtype, lead, K)
     if "x" in want and grad_x is None:
-        grad_x = x.new_empty(x.shape)
+        grad_x, gxr = _dense_new(x, lead, K)
     if "W" in want and grad_W is None:
         grad_W = x.new_empty((K, N))
     if "bias" in want and grad_bias is None:
         grad_bias = x.new_empty(N)
-    gxr = _dense_rows(grad_x, "grad_x", dtype, lead, K)
     gWp, gbp = _dense_vector(grad_W, "grad_W", dtype, K, N), _dense_vector(grad_bias, "grad_bias", dtype, N)
     index = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
@@ -673,13 +678,11 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     if out is not None or mean is not None or rstd is not None:
         _dense_outputs([("out", out), ("mean", mean), ("rstd", rstd)], [("x", x), ("weight", weight), ("bias", bias)],
                        {("out", "x")})
-    if out is None:
-        out = x.new_empty((*lead, C))
+    out, orow = (out, _dense_rows(out, "out", dtype, lead, C)) if out is not None else _dense_new(x, lead, C)
     if mean is None:
         mean = x.new_empty(lead, dtype=torch.float32)
     if rstd is None:
-        rstd = x.new_empty(lead, dtype=torch.float32)
-    orow = _dense_rows(out, "out", dtype, lead, C)
+        rstd = torch.empty_like(mean) if mean.is_contiguous() else x.new_empty(lead, dtype=torch.float32)
     mp, rp = _dense_vector(mean, "mean", torch.float32, *lead), _dense_vector(rstd, "rstd", torch.float32, *lead)
     index = _dense_device(x, weight, bias, out, mean, rstd)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
@@ -713,13 +716,13 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
         _dense_outputs([("grad_x", grad_x), ("grad_weight", grad_weight), ("grad_bias", grad_bias)],
                        [("x", x), ("weight", weight), ("mean", mean), ("rstd", rstd), ("grad_out", grad_out)],
                        {("grad_x", "x"), ("grad_x", "grad_out")})
-    if "x" in want and grad_x is None:
-        grad_x = x.new_empty(x.shape)
-    if "weight" in want and grad_weight is None:
-        grad_weight = x.new_empty(C)
-    if "bias" in want and grad_bias is None:
-        grad_bias = x.new_empty(C)
     gxr = _dense_rows(grad_x, "grad_x", dtype, lead, C)
+    if "x" in want and grad_x is None:
+        grad_x, gxr = _dense_new(x, lead, C)
+    if "weight" in want and grad_weight is None:
+        grad_weight = x.new_empty(C) if weight is None else torch.empty_like(weight)
+    if "bias" in want and grad_bias is None:
+        grad_bias = x.new_empty(C) if grad_weight is None else torch.empty_like(grad_weight)
     gwp, gbp = _dense_vector(grad_weight, "grad_weight", dtype, C), _dense_vector(grad_bias, "grad_bias", dtype, C)
     index = _dense_device(x, weight, mean, rstd, grad_out, grad_x, grad_weight, grad_bias, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)

@@ -93,8 +93,9 @@ typedef enum {
     ETP_ERR_BAD_CSR = 3,     /* reserved for callers that map the validation flag      */
     ETP_ERR_CUDA = 4,        /* a CUDA launch or query failed                           */
     ETP_ERR_ALLOC = 5,       /* host allocation of a plan failed                        */
-    ETP_ERR_WORKSPACE = 6,   /* workspace smaller than etp_reverse_csr_workspace_size   */
-    ETP_ERR_TOO_LARGE = 7    /* N or E above the fixed scratch of the _static variant   */
+    ETP_ERR_WORKSPACE = 6,   /* workspace smaller than the call's size function says    */
+    ETP_ERR_TOO_LARGE = 7    /* sizes above the fixed scratch of the _static variant, or
+                                rows above a dense operator's limit                     */
 } etp_status;
 
 /* Bits of the flag written by etp_validate_csr. */
