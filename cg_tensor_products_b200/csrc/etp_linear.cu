@@ -394,7 +394,7 @@ __device__ __forceinline__ Item item_of(const Job& j, int i, int bn) {
         it.split = (int)j.tiles.quot(i);
         tile = i - it.split * j.tiles.d;
         it.k0 = it.split * j.range;
-        it.k1 = min(j.k, it.k0 + j.range);
+        it.k1 = j.k - it.k0 < j.range ? j.k : it.k0 + j.range;  // k0 + range may pass 2^31
     }
     const int mt = (int)j.ntn.quot(tile);
     it.m0 = mt * kRowsTile * MT;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
     const int step = keep_a ? 1 : gridDim.x;
     const int lo = keep_a ? (int)((long long)job.items * blockIdx.x / gridDim.x) : blockIdx.x;
     const int hi = keep_a ? (int)((long long)job.items * (blockIdx.x + 1) / gridDim.x) : job.items;
-    if (P == Product::kGradW) launch_dependents();
+    if (P == Product::kGradW && (job.part || job.bias_part)) launch_dependents();
     if (IMAGE) wait_for_previous();  // for the image
 
     if (warp >= W::kEpi && warp < W::kMma) {  // loaders
@@ -1133,10 +1133,12 @@ Ranges ranges(bool bf16, int M, int K, int N) {
     const int stages = (M + kRangeK - 1) / kRangeK;
     int want = r.tiles < sms ? sms / r.tiles : 1;
     want = want < stages ? want : stages;
-    const int least = (M + kMostRange - 1) / kMostRange;
+    const int least = bf16 ? (int)(((long long)M + kMostRange - 1) / kMostRange) : 1;
     want = want > least ? want : least;
     const int per = want > 0 ? (stages + want - 1) / want : 1;
-    r.range = per * kRangeK;
+    // a multiple of kRangeK that an int holds (M is below 2^31 - 128)
+    const long long range = (long long)per * kRangeK, most = (1ll << 31) - kRangeK;
+    r.range = (int)(range < most ? range : most);
     r.splits = stages > 0 ? (stages + per - 1) / per : 0;
     return r;
 }

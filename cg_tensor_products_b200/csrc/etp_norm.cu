@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ float red[kWarps];
     extern __shared__ float acc[];  // [2][C], warp teams with PARAMS
     constexpr int U = kRowsAtOnce<V, NV> > 2 ? 2 : kRowsAtOnce<V, NV>;
-    launch_dependents();
+    if (PARAMS) launch_dependents();
     const int step = BLOCK ? kThreads : team;
     const int lane = threadIdx.x & (step - 1);
     const int rows_per_block = kThreads / step;

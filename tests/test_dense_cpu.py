@@ -92,11 +92,16 @@ def test_linear_backward_refusals(lib):
     f = lib.etp_linear_workspace_size
     assert f(0, 4, 2, 8, 8, 0, ctypes.byref(size)) == OK
     assert f(0, 4, 2, 8, 8, 1, ctypes.byref(size)) == OK and size.value > 0
+    need = size.value
     assert f(0, 4, 2, 8, 8, 1, None) == f(0, -1, 2, 8, 8, 1, ctypes.byref(size)) == BAD
     assert f(0, 4, 2, 8, 8, 2, ctypes.byref(size)) == BAD
     assert f(0, 4, 2, 0, 8, 0, ctypes.byref(size)) == f(0, 4, 2, 8, 0, 1, ctypes.byref(size)) == BAD
     assert f(5, 4, 2, 8, 8, 0, ctypes.byref(size)) == UNSUP
     assert f(0, 1 << 20, 1 << 11, 8, 8, 0, ctypes.byref(size)) == LARGE
+
+    for dtype in (0, 1):  # the most rows that a call takes: sizes that do not wrap around
+        assert f(dtype, (1 << 31) - 129, 1, 4, 4, 1, ctypes.byref(size)) == OK and 0 < size.value < 1 << 30
+        assert f(dtype, (1 << 31) - 128, 1, 4, 4, 1, ctypes.byref(size)) == LARGE
 
     def call(dtype=0, groups=4, per=2, K=8, N=8, x=rows(), W=p, act=1, z=rows(), g=rows(), gx=rows(), gW=p, gb=p,
              ws=p, n=1 << 40):
@@ -108,7 +113,7 @@ def test_linear_backward_refusals(lib):
     assert call(gx=rows(rs=7)) == call(gx=rows(PTR + 2)) == BAD
     assert call(gW=ctypes.c_void_p(PTR + 2)) == call(gb=ctypes.c_void_p(PTR + 1)) == BAD
     assert call(ws=None) == call(ws=ctypes.c_void_p(PTR + 4)) == BAD
-    assert call(n=0) == call(n=size.value - 1) == WS
+    assert call(n=0) == call(n=need - 1) == WS
     assert call(gx=None, gW=None, gb=None, x=None, W=None, z=None, g=None) == OK  # nothing wanted
     assert call(groups=1 << 20, per=1 << 11) == LARGE
 

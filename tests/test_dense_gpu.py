@@ -309,6 +309,36 @@ def test_streams_and_captured_graphs():
         assert all(torch.equal(a, c) for a, c in zip(outs[i], ref))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_far_rows_and_many_rows(dtype):
+    """Rows whose offsets pass 2^32 elements, and the most rows that a call takes (one row used for all of them)."""
+    normal = _rand(13)
+    stride = (1 << 31) - 64
+    big = torch.empty(2 * stride + 128, device="cuda", dtype=dtype)
+    far = big.as_strided((3, 64), (stride, 1))
+    x = normal(3, 64, dtype=dtype)
+    far.copy_(x)
+    W = normal(64, 48, dtype=dtype)
+    assert torch.equal(etp.linear_forward(far, W), etp.linear_forward(x, W))
+    assert torch.equal(etp.layer_norm_forward(far)[0], etp.layer_norm_forward(x)[0])
+    g = normal(3, 48, dtype=dtype)
+    assert torch.equal(etp.linear_backward(far, W, g)[1], etp.linear_backward(x, W, g)[1])
+    etp.linear_backward(x, W, g, want=("x",), grad_x=far)
+    assert torch.equal(far, etp.linear_backward(x, W, g, want=("x",))[0])
+    del big, far
+    # sums of ones are exact in each range (below 2^24 terms each); joining at most 512 ranges rounds 512 times by
+    # 2^-24 of a sum that never exceeds the last
+    M = (1 << 31) - 129
+    one = torch.ones(1, 4, device="cuda", dtype=dtype).expand(M, 4)
+    _, gW, gb = etp.linear_backward(one, torch.ones(4, 4, device="cuda", dtype=dtype), one, want=("W", "bias"))
+    tol = 2.0**-15 + torch.finfo(dtype).eps / 2
+    assert bool(((gW.double() / M - 1).abs() <= tol).all()) and bool(((gb.double() / M - 1).abs() <= tol).all())
+    assert etp.device_fault() == 0
+    with pytest.raises(etp.EtpError):
+        etp.linear_backward(one[:1].expand(M + 1, 4), torch.ones(4, 4, device="cuda", dtype=dtype),
+                            one[:1].expand(M + 1, 4), want=("W",))
+
+
 def test_two_calls_at_once():
     """Calls on two streams that overlap on the GPU, each with its own workspace."""
     normal = _rand(12)
