@@ -478,6 +478,22 @@ def _dense_new(x, lead, C: int):
     return t, ctypes.byref(_Rows(t.data_ptr(), C if len(lead) == 1 else lead[1] * C, C))
 
 
+def _dense_code(dtype):
+    """etp_dtype of a torch dtype or its name."""
+    code = _DENSE_TYPES.get("torch." + str(dtype).replace("torch.", ""))
+    if code is None:
+        raise ValueError(f"dtype: expected float32 or bfloat16, got {dtype}")
+    return code
+
+
+def _dense_index(device):
+    """Index of a CUDA device (None, or one without an index: the current one)."""
+    import torch
+
+    index = None if device is None else torch.device(device).index
+    return torch.cuda.current_device() if index is None else index
+
+
 def _dense_type(x):
     code = _DENSE_TYPES.get(str(x.dtype))
     if code is None:
@@ -537,8 +553,9 @@ def _dense_bytes(index: int, name: str, *args) -> int:
     return b.value
 
 
-def _dense_workspace(index: int, workspace, name: str, *args):
-    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any."""
+def _dense_workspace(index: int, workspace, stream, name: str, *args):
+    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any. A new one
+    belongs to the call's stream: its memory is given to later work of that stream alone."""
     if workspace is not None:
         _expect(workspace, "workspace", "uint8", (None,))
         if not workspace.is_contiguous():
@@ -549,7 +566,10 @@ def _dense_workspace(index: int, workspace, name: str, *args):
         return None, 0
     import torch
 
-    return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
 
 
 def _span(t):
@@ -598,10 +618,8 @@ def _check_linear(x, W, activation):
 
 def linear_workspace_size(M: int, K: int, N: int, dtype="float32", backward: bool = False, device=None) -> int:
     """Bytes of workspace linear_forward (linear_backward) needs for M rows (etp_linear_workspace_size on `device`)."""
-    import torch
-
-    index = torch.device(device).index if device is not None else torch.cuda.current_device()
-    return _dense_bytes(index, "etp_linear_workspace_size", _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")],
+    index = _dense_index(device)
+    return _dense_bytes(index, "etp_linear_workspace_size", _dense_code(dtype),
                         int(M), 1, int(K), int(N), int(bool(backward)))
 
 
@@ -626,7 +644,7 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     z, zr = (z, _dense_rows(z, "z", dtype, lead, N)) if z is not None or not save_z else _dense_new(x, lead, N)
     index = _dense_device(x, W, bias, residual, z, out, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
-    workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 0)
+    workspace, nbytes = _dense_workspace(index, workspace, stream, "etp_linear_workspace_size", code, groups, per, K, N, 0)
     _dense_call(index, "etp_linear_forward", _load().etp_linear_forward, code, groups, per, K, N, xr, Wp, bp, act, rr,
                 zr, orow, _ptr(workspace), nbytes, stream=stream)
     return out if z is None else (out, z)
@@ -659,7 +677,7 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
     gWp, gbp = _dense_vector(grad_W, "grad_W", dtype, K, N), _dense_vector(grad_bias, "grad_bias", dtype, N)
     index = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
-    workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 1)
+    workspace, nbytes = _dense_workspace(index, workspace, stream, "etp_linear_workspace_size", code, groups, per, K, N, 1)
     _dense_call(index, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, xr, Wp, act, zr, gr,
                 gxr, gWp, gbp, _ptr(workspace), nbytes, stream=stream)
     return grad_x, grad_W, grad_bias
@@ -693,11 +711,9 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
 
 def layer_norm_workspace_size(M: int, C: int, dtype="float32", device=None) -> int:
     """Bytes of workspace layer_norm_backward needs for M rows (etp_layer_norm_workspace_size on `device`)."""
-    import torch
-
-    index = torch.device(device).index if device is not None else torch.cuda.current_device()
+    index = _dense_index(device)
     return _dense_bytes(index, "etp_layer_norm_workspace_size",
-                        _DENSE_TYPES["torch." + str(dtype).replace("torch.", "")], int(M), 1, int(C))
+                        _dense_code(dtype), int(M), 1, int(C))
 
 
 def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "bias"), grad_x=None, grad_weight=None,
@@ -728,7 +744,7 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
     nbytes = 0
     if grad_weight is not None or grad_bias is not None:
-        workspace, nbytes = _dense_workspace(index, workspace, "etp_layer_norm_workspace_size", code, groups, per, C)
+        workspace, nbytes = _dense_workspace(index, workspace, stream, "etp_layer_norm_workspace_size", code, groups, per, C)
     _dense_call(index, "etp_layer_norm_backward", _load().etp_layer_norm_backward, code, groups, per, C, xr, wp,
                 mp, rp, gr, gxr, gwp, gbp, _ptr(workspace) if nbytes else None, nbytes, stream=stream)
     return grad_x, grad_weight, grad_bias

@@ -310,6 +310,45 @@ def test_streams_and_captured_graphs():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 64, 40000), (100, 130, 19999), (129, 200, 38016), (1000, 96, 9480)])
+def test_linear_few_rows_many_columns(M, K, N, dtype):
+    """Several column tiles a CTA, with W converted by it and ahead of it; the transposed sizes have grad_x do the same."""
+    normal = _rand(17)
+    for k, n in ((K, N), (N, K)):
+        x, W, b, g = (normal(*s, dtype=dtype) for s in ((M, k), (k, n), (n,), (M, n)))
+        _check_linear(x, W, b, "silu", None, g)
+
+
+def test_own_workspace_on_another_stream():
+    """The workspace that a call allocates for another stream is not handed to the current one while the call runs."""
+    normal = _rand(19)
+    x, W, g = normal(20000, 256), normal(256, 256), normal(20000, 256)
+    gamma = normal(256)
+    _, mean, rstd = etp.layer_norm_forward(x, gamma)
+    want = (etp.linear_forward(x, W), *etp.linear_backward(x, W, g), *etp.layer_norm_backward(x, gamma, mean, rstd, g))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    need = [etp.linear_workspace_size(20000, 256, 256, "float32", b) for b in (False, True)]
+    need.append(etp.layer_norm_workspace_size(20000, 256))
+    runs = [lambda: (etp.linear_forward(x, W, stream=s),), lambda: etp.linear_backward(x, W, g, stream=s),
+            lambda: etp.layer_norm_backward(x, gamma, mean, rstd, g, stream=s)]
+    got = []
+    for run, n in zip(runs, need):
+        assert n > 0
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(2_000_000)
+        got += run()
+        junk = [torch.full((n,), 0xFF, device="cuda", dtype=torch.uint8) for _ in range(3)]
+        torch.cuda.synchronize()
+        del junk
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        etp.linear_workspace_size(4, 4, 4, "float16")
+    assert etp.linear_workspace_size(20000, 256, 256, device="cuda") == need[0]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_far_rows_and_many_rows(dtype):
     """Rows whose offsets pass 2^32 elements, and the most rows that a call takes (one row used for all of them)."""
     normal = _rand(13)
