@@ -1080,7 +1080,11 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
 // tiled: the widest tile that still gives every SM one, or the narrowest (256 columns
 // with bfloat16 alone: A is then read, and dz formed, half as often; 131072 x 256 -> 256
 // grad_x 102 us with 128, 61 us with 256; float32 parts leave no tensor memory for it); and whether W
-// is converted ahead (an image), which pays once a CTA would convert it more than once.
+// is converted ahead (an image), which pays once a CTA would convert it more than once and
+// enough row tiles share it. float32, with the image / without: 64 x 256 -> 65536 64 / 51 us,
+// 256 x 1024 -> 32768 155 / 170, 4096 x 512 -> 4096 90 / 156. bfloat16, whose image is only a
+// copy in another order: 64 x 2048 -> 40960 120 / 57 us, 1024 x 1024 -> 8192 49 / 43,
+// 4096 x 512 -> 4096 43 / 43, 16384 x 256 -> 2048 47 / 49.
 struct Tiling {
     int bn;
     bool image;
@@ -1091,7 +1095,7 @@ Tiling tiling(bool bf16, Product p, int M, int k, int n) {
     const int sms = sm_count();
     Tiling t;
     t.bn = bf16 && p == Product::kGradX && n > 128 && mt * ((n + 255) / 256) >= sms ? 256 : n > 64 && mt * ((n + 127) / 128) >= sms ? 128 : n > 32 && mt * ((n + 63) / 64) >= sms ? 64 : 32;
-    t.image = mt * ((n + t.bn - 1) / t.bn) >= 2 * sms;
+    t.image = mt >= (bf16 ? 32 : 2) && mt * ((n + t.bn - 1) / t.bn) >= 2 * sms;
     constexpr int K = 64;  // k of a stage of either
     static_assert(kStageK<float, Product::kForward> == K && kStageK<float, Product::kGradX> == K, "image tiles");
     const size_t part = (size_t)(p == Product::kForward && t.bn < 64 ? 64 : t.bn) * K * 2;
