@@ -319,6 +319,32 @@ def test_linear_few_rows_many_columns(M, K, N, dtype):
         _check_linear(x, W, b, "silu", None, g)
 
 
+def test_linear_largest_matrix():
+    """W and grad_W of the most channels: offsets up to 2^32 elements."""
+    n, dtype = 65536, torch.bfloat16
+    normal = _rand(23)
+    x, g = normal(2, n, dtype=dtype), normal(2, n, dtype=dtype)
+    W = torch.zeros(n, n, device="cuda", dtype=dtype)
+    rows, cols = [0, 1, 32767, 32768, 65534, 65535], [0, 63, 32768, 65535]
+    W[rows] = normal(len(rows), n, dtype=dtype)
+    out = etp.linear_forward(x, W)
+    want = x[:, rows].double() @ W[rows].double()
+    slack = x[:, rows].double().abs() @ W[rows].double().abs()
+    assert bool(((out.double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-20 * slack).all())
+    gx, gW, _ = etp.linear_backward(x, W, g, want=("x", "W"))
+    want, slack = g.double() @ W[rows].double().T, g.double().abs() @ W[rows].double().abs().T
+    # 65536 terms in float32 accumulators that truncate: a relative 2^-23 of the sum of magnitudes for each 16 terms
+    assert bool(((gx[:, rows].double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-11 * slack).all())
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[rows] = False
+    assert not bool(gx[:, rest].any())
+    for a, b in ((rows, slice(None)), (slice(None), cols)):
+        want = x.double().T[a] @ g.double()[:, b]
+        slack = x.double().T[a].abs() @ g.double()[:, b].abs()
+        assert bool(((gW[a, b].double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-20 * slack).all())
+    assert etp.device_fault() == 0
+
+
 def test_own_workspace_on_another_stream():
     """The workspace that a call allocates for another stream is not handed to the current one while the call runs."""
     normal = _rand(19)
