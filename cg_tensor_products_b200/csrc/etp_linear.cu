@@ -1079,7 +1079,10 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
 // How the forward and grad_x products of M rows, k contracted and n output columns are
 // tiled: the widest tile that still gives every SM one, or the narrowest (256 columns
 // with bfloat16 alone: A is then read, and dz formed, half as often; 131072 x 256 -> 256
-// grad_x 102 us with 128, 61 us with 256; float32 parts leave no tensor memory for it); and whether W
+// grad_x 102 us with 128, 61 us with 256; float32 parts leave no tensor memory for it).
+// float32 takes 128 columns once every SM gets two such tiles: below that its one or two
+// rounds wait for whole conversions (20480 x 128 -> 128 22.6 us with 128, 17.7 us with 64,
+// 37000 rows 24.6 / 21.5, 40000 rows 21.5 / 23.5; bfloat16 12.3 / 13.3 at 20480). And whether W
 // is converted ahead (an image), which pays once a CTA would convert it more than once and
 // enough row tiles share it. float32, with the image / without: 64 x 256 -> 65536 64 / 51 us,
 // 256 x 1024 -> 32768 155 / 170, 4096 x 512 -> 4096 90 / 156. bfloat16, whose image is only a
@@ -1094,7 +1097,11 @@ Tiling tiling(bool bf16, Product p, int M, int k, int n) {
     const long long mt = ((long long)M + kRowsTile - 1) / kRowsTile;
     const int sms = sm_count();
     Tiling t;
-    t.bn = bf16 && p == Product::kGradX && n > 128 && mt * ((n + 255) / 256) >= sms ? 256 : n > 64 && mt * ((n + 127) / 128) >= sms ? 128 : n > 32 && mt * ((n + 63) / 64) >= sms ? 64 : 32;
+    auto enough = [&](int bn, int each) { return n > bn / 2 && mt * ((n + bn - 1) / bn) >= (long long)each * sms; };
+    t.bn = bf16 && p == Product::kGradX && enough(256, 1) ? 256
+           : enough(128, bf16 ? 1 : 2)                    ? 128
+           : enough(64, 1)                                ? 64
+                                                          : 32;
     t.image = mt >= (bf16 ? 32 : 2) && mt * ((n + t.bn - 1) / t.bn) >= 2 * sms;
     constexpr int K = 64;  // k of a stage of either
     static_assert(kStageK<float, Product::kForward> == K && kStageK<float, Product::kGradX> == K, "image tiles");
