@@ -26,10 +26,13 @@
 // The tensor core truncates when it adds to its accumulator; so a float32 stage starts
 // a new accumulator, adds the small products first and the x0 w0 ones last (up to four
 // truncated additions of full size), and stages are added up in registers, rounded to
-// nearest. bfloat16 operands are one part (dz is rounded to it: the tensor core reads
-// nothing wider beside bf16 weights without a second product); their accumulator holds a
-// whole tile: up to 2^16 k in 4096 truncated additions, each 2^-24 of the sum on average,
-// stay below a sixteenth of the result's own rounding.
+// nearest. bfloat16 operands are one part. dz of a bfloat16 layer with an activation is not
+// a bfloat16 value: it enters as two rounded parts, its upper 16 bits (one part alone, 2^-8
+// of each dz, takes grad_x from 58.7 to 56.3 us at 131072 x 256 -> 256 and lifts the
+// gradients' error from 1.65e-3, that of storing them, to 2.35e-3). A bfloat16
+// accumulator holds a whole tile: up to 2^16 k in 4096 truncated additions (8192 with dz's
+// low part), each 2^-24 of the sum on average, stay below an eighth of the result's own
+// rounding.
 //
 // grad_W contracts over the rows: the rows are cut into as many ranges as leave every
 // SM one, each range's sums go to the workspace, and a second launch adds them up in
@@ -72,8 +75,12 @@ struct Int {
     static constexpr int value = V;
 };
 
-template <typename T>
-constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+// bfloat16 parts of an operand: three of a float32 one, two of the dz of bfloat16 layers
+// (computed in float32; two parts are within 2^-17 of it, one within 2^-8), one of the rest.
+template <typename T, Product P>
+constexpr int kPartsA = sizeof(T) == 4 ? 3 : P == Product::kGradX ? 2 : 1;
+template <typename T, Product P>
+constexpr int kPartsB = sizeof(T) == 4 ? 3 : P == Product::kGradW ? 2 : 1;
 // k of a stage. grad_W's float32 stages are half as long: they hold three operands.
 template <typename T, Product P>
 constexpr int kStageK = sizeof(T) == 4 && P == Product::kGradW ? 32 : 64;
@@ -130,8 +137,9 @@ struct Layout {
     // A slot: B's parts and an A that is used as it is; a converted A's parts have columns in tensor memory
     static constexpr uint32_t kAPart = kTmemA ? 0 : MT * kRowsTile * kK * 2;
     static constexpr uint32_t kBPart = (kBMn && BN < 64 ? 64u : (uint32_t)BN) * kK * 2;
-    static constexpr uint32_t kSlot = kParts<T> * kBPart + kAPart;
-    static constexpr uint32_t kACols = kTmemA ? kParts<T> * kK / 2 : 0;
+    static constexpr int kPA = kPartsA<T, P>, kPB = kPartsB<T, P>;
+    static constexpr uint32_t kSlot = kPB * kBPart + kAPart;
+    static constexpr uint32_t kACols = kTmemA ? kPA * kK / 2 : 0;
     // Elements on their way, per stage: of A, of the pre-activation beside dz, of B
     static constexpr uint32_t kRawA = kTmemA ? kRowsTile * kK * sizeof(T) : 0;
     static constexpr uint32_t kRawB = kConvB ? ShareB::kIters * W::kLoaders * 8 * sizeof(T) : 0;
@@ -145,11 +153,15 @@ struct Layout {
     static constexpr int kFew = kTmemSlots < kSome ? kTmemSlots : kSome;
     // Stages in flight. Copies straight into a slot share their groups, and the slot's hand-over lags behind by
     // as many; without other elements on their way they use the slots themselves.
-    static constexpr int kMost = !kTmemA || kCopyB ? kFew - 1 : 3;
+    // grad_W of bfloat16 has large slots (two parts of dz): one stage ahead and three slots are fastest (131072 x 128 ->
+    // 128 38 us, with four slots 44 us, two stages ahead 48 us; 256 -> 256 with stages of half the length 83 us, 67 us so).
+    static constexpr bool kBig = kDzB && sizeof(T) == 2;
+    static constexpr int kMost = kBig ? 1 : !kTmemA || kCopyB ? kFew - 1 : 3;
     static constexpr int kRoom = kRaw ? (int)((kSmemMost - kTail - kFew * kSlot) / kRaw) : 1;
     static constexpr int kDepth = kRoom < kMost ? kRoom : kMost;
     static constexpr int kFit = (int)((kSmemMost - kTail - kDepth * kRaw) / kSlot);
-    static constexpr int kCap = kTmemSlots < (kRaw ? kWant + 1 : 6) ? kTmemSlots : (kRaw ? kWant + 1 : 6);
+    static constexpr int kMostSlots = kBig ? kWant : kRaw ? kWant + 1 : 6;
+    static constexpr int kCap = kTmemSlots < kMostSlots ? kTmemSlots : kMostSlots;
     static constexpr int kSlots = kFit < kCap ? kFit : kCap;
     static constexpr int kLag = kTmemA && !kCopyB ? 0 : kRaw ? kDepth : kSlots / 2;  // the rest: ready for the MMAs
     static constexpr uint32_t kOffRaw = kSlots * kSlot;
@@ -261,37 +273,30 @@ __device__ __forceinline__ void read16(const unsigned char* p, float* v) {
 __device__ __forceinline__ uint32_t high_pair(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float high_part(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
 // The parts of N floats, part after part, as bf16 pairs: emit(p, pairs). Three truncated
-// parts of a float32 operand, one rounded part of a bf16 one.
-template <typename T, int N, typename Emit>
+// parts of a float32 operand, or NP rounded parts, each of what is left by those before it.
+template <typename T, int NP, int N, typename Emit>
 __device__ __forceinline__ void split_parts(float (&v)[N], Emit&& emit) {
     uint32_t w[N / 2];
-    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < N; j += 2) w[j / 2] = pack_bf16(v[j], v[j + 1]);
-        emit(0, w);
-    } else {
+    for (int p = 0; p < NP; ++p) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
+        for (int j = 0; j < N; j += 2) w[j / 2] = sizeof(T) == 4 ? high_pair(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
+        emit(p, w);
+        if (p + 1 < NP)
 #pragma unroll
-            for (int j = 0; j < N; j += 2) w[j / 2] = high_pair(v[j], v[j + 1]);
-            emit(p, w);
-            if (p < 2)
-#pragma unroll
-                for (int j = 0; j < N; j += 2) {  // packed: v - high_part(v), exact
-                    const float2 r = __ffma2_rn(make_float2(high_part(v[j]), high_part(v[j + 1])),
-                                                make_float2(-1.f, -1.f), make_float2(v[j], v[j + 1]));
-                    v[j] = r.x, v[j + 1] = r.y;
-                }
-        }
+            for (int j = 0; j < N; j += 2) {  // packed: v - part, exact
+                const float2 r = __ffma2_rn(make_float2(bf16_lo(w[j / 2]), bf16_hi(w[j / 2])), make_float2(-1.f, -1.f),
+                                            make_float2(v[j], v[j + 1]));
+                v[j] = r.x, v[j + 1] = r.y;
+            }
     }
 }
-template <typename T>
-__device__ __forceinline__ void store_parts(unsigned char* dst, uint32_t part, float (&v)[8]) {
-    split_parts<T, 8>(v, [&](int p, const uint32_t(&w)[4]) {
-        *reinterpret_cast<uint4*>(dst + p * part) = make_uint4(w[0], w[1], w[2], w[3]);
+template <typename T, int NP>
+__device__ __forceinline__ void store_parts(unsigned char* dst, uint32_t part, float (&v)[8], bool low = true) {
+    split_parts<T, NP, 8>(v, [&](int p, const uint32_t(&w)[4]) {
+        if (p == 0 || low) *reinterpret_cast<uint4*>(dst + p * part) = make_uint4(w[0], w[1], w[2], w[3]);
     });
 }
 
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
     using W = Warps<T, P>;
     using ShareA = typename Lay::ShareA;
     using ShareB = typename Lay::ShareB;
-    constexpr int NP = kParts<T>, K = Lay::kK, kSlots = Lay::kSlots, kRing = Lay::kRing;
+    constexpr int K = Lay::kK, kSlots = Lay::kSlots, kRing = Lay::kRing;
     constexpr bool kDzA = Lay::kDzA, kDzB = Lay::kDzB;
 
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -618,8 +623,8 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
                         }
                     }
                 }
-                split_parts<T, kB>(v, [&](int p, const uint32_t(&w)[kB / 2]) {
-                    tc::tmem_st(col + p * (K / 2) + b * (kB / 2), w);
+                split_parts<T, Lay::kPA, kB>(v, [&](int p, const uint32_t(&w)[kB / 2]) {
+                    if (sizeof(T) == 4 || p == 0 || job.silu) tc::tmem_st(col + p * (K / 2) + b * (kB / 2), w);
                 });
             }
         };
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
 #pragma unroll
                     for (int j = 0; j < 8; ++j) bsum[j] += v[j];
                 }
-                if (ShareB::has(lt, i)) store_parts<T>(sb + ShareB::offset(lt, i), Lay::kBPart, v);
+                if (ShareB::has(lt, i)) store_parts<T, Lay::kPB>(sb + ShareB::offset(lt, i), Lay::kBPart, v, sizeof(T) == 4 || job.silu);
             }
         };
         // -- operands used as they are, straight into the slot
@@ -712,12 +717,12 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
             if (n >= kSlots && !wait(&empty[slot], (n / kSlots - 1) & 1)) break;
             if (Lay::kTmemA) tc::fence_after_sync();
             unsigned char* sb = smem + slot * Lay::kSlot;
-            unsigned char* sa = sb + NP * Lay::kBPart;
+            unsigned char* sa = sb + Lay::kPB * Lay::kBPart;
             if (IMAGE && lt == 0) {
                 const int nks = (job.k + K - 1) / K;
-                tc::mbar_expect_tx(&bfull[slot], NP * Lay::kBPart);
-                tc::bulk_g2s(sb, job.image + (size_t)((now.it.n0 / BN) * nks + now.ks) * (NP * Lay::kBPart),
-                             NP * Lay::kBPart, &bfull[slot]);
+                tc::mbar_expect_tx(&bfull[slot], Lay::kPB * Lay::kBPart);
+                tc::bulk_g2s(sb, job.image + (size_t)((now.it.n0 / BN) * nks + now.ks) * (Lay::kPB * Lay::kBPart),
+                             Lay::kPB * Lay::kBPart, &bfull[slot]);
                 images = n + 1;
             }
             const int kk = now.it.k0 + now.ks * K;
@@ -776,24 +781,26 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
         constexpr uint32_t idesc = idesc_bf16<Lay::kAMn && !Lay::kTmemA, Lay::kBMn>(BN);
         // one K step of 16, one part: descriptor units of 16 bytes
         constexpr uint32_t kStepA = (Lay::kAMn ? 2048 : 32) >> 4, kStepB = (Lay::kBMn ? 2048 : 32) >> 4;
-        constexpr int kPairs = NP == 3 ? 6 : 1;
-        constexpr int pa[6] = {NP == 3 ? 1 : 0, 0, 2, 0, 1, 0}, pb[6] = {NP == 3 ? 1 : 0, 2, 0, 1, 0, 0};
+        // the part products, smallest first: six of float32; the low and the high part of a bfloat16 layer's dz
+        constexpr bool kF32 = sizeof(T) == 4;
+        constexpr int kPairs = kF32 ? 6 : kDzA || kDzB ? 2 : 1;
+        constexpr int pa[6] = {kF32 || kDzA ? 1 : 0, 0, 2, 0, 1, 0}, pb[6] = {kF32 || kDzB ? 1 : 0, kF32 ? 2 : 0, 0, 1, 0, 0};
         uint64_t base_a = 0;
-        if constexpr (!Lay::kTmemA) base_a = operand_desc<Lay::kAMn, K>(tc::smem_u32(smem + NP * Lay::kBPart));
+        if constexpr (!Lay::kTmemA) base_a = operand_desc<Lay::kAMn, K>(tc::smem_u32(smem + Lay::kPB * Lay::kBPart));
         const uint64_t base_b = operand_desc<Lay::kBMn, K>(tc::smem_u32(smem));
         // the stage's MMAs, unrolled: operand addresses are the slot's plus constants
-        auto issue = [&](auto steps_c, uint32_t d, int slot, int aslot, bool first) {
-            constexpr int S = decltype(steps_c)::value;
+        auto issue = [&](auto steps_c, auto from_c, uint32_t d, int slot, int aslot, bool first) {
+            constexpr int S = decltype(steps_c)::value, kFrom = decltype(from_c)::value;
             const uint64_t db = base_b + (uint64_t)(slot * (Lay::kSlot >> 4));
             [[maybe_unused]] const uint64_t da = base_a + (uint64_t)(slot * (Lay::kSlot >> 4));
             [[maybe_unused]] const uint32_t ta = tmem_a + aslot * Lay::kACols;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int q = 0; q < kPairs; ++q)
+                for (int q = kFrom; q < kPairs; ++q)
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
-                        const uint32_t acc = q == 0 && s == 0 ? (first ? 0u : 1u) : 1u;
+                        const uint32_t acc = q == kFrom && s == 0 ? (first ? 0u : 1u) : 1u;
                         const uint64_t b = db + (uint64_t)(pb[q] * (Lay::kBPart >> 4) + s * kStepB);
                         if constexpr (Lay::kTmemA)
                             mma_bf16_ta(d, ta + pa[q] * (K / 2) + s * 8, b, idesc, acc);
@@ -819,14 +826,20 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
                 const int left = it.k1 - it.k0 - ks * K;
                 const uint32_t d = tmem + buf * Lay::kAcc;
                 const int aslot = keep_a ? block % kSlots : slot;
-                if (left > K - 16)
-                    issue(Int<K / 16>{}, d, slot, aslot, first);
-                else if (K == 64 && left > 32)
-                    issue(Int<K == 64 ? 3 : 1>{}, d, slot, aslot, first);
-                else if (K == 64 && left > 16)
-                    issue(Int<K == 64 ? 2 : 1>{}, d, slot, aslot, first);
+                auto steps = [&](auto from_c) {
+                    if (left > K - 16)
+                        issue(Int<K / 16>{}, from_c, d, slot, aslot, first);
+                    else if (K == 64 && left > 32)
+                        issue(Int<K == 64 ? 3 : 1>{}, from_c, d, slot, aslot, first);
+                    else if (K == 64 && left > 16)
+                        issue(Int<K == 64 ? 2 : 1>{}, from_c, d, slot, aslot, first);
+                    else
+                        issue(Int<1>{}, from_c, d, slot, aslot, first);
+                };
+                if (kPairs == 2 && !job.silu)  // dz is the bfloat16 cotangent itself: no low part
+                    steps(Int<kPairs == 2 ? 1 : 0>{});
                 else
-                    issue(Int<1>{}, d, slot, aslot, first);
+                    steps(Int<0>{});
                 tc::mma_commit(&empty[slot]);
                 if (ks + 1 == it.stages || (ks + 1) % kChunk<T> == 0) {
                     tc::mma_commit(&tfull[buf]);
@@ -952,8 +965,8 @@ __global__ void __launch_bounds__(256) etp_linear_image_kernel(const T* __restri
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < left ? to_float(p[j]) : 0.f;
-    store_parts<T>(image + (size_t)tile * kParts<T> * Lay::kBPart + chunk_offset<Lay::kK>(r, c), Lay::kBPart,
-                   v);
+    store_parts<T, Lay::kPB>(image + (size_t)tile * Lay::kPB * Lay::kBPart + chunk_offset<Lay::kK>(r, c),
+                             Lay::kBPart, v);
 }
 
 // grad_W from the ranges' sums [splits][count] and grad_bias from [bias_rows][N], both in

@@ -20,9 +20,9 @@
  *
  * Types. All operands of a call have one type, ETP_F32 or ETP_BF16; mean and rstd
  * of the layer norm are float32. Sums, statistics and activations are computed in
- * float32 and rounded once when stored; one more rounding is the backward's dz of
- * ETP_BF16 operands, which enters the products of grad_x and grad_W as bfloat16 (as it
- * would if it were stored; grad_bias sums it unrounded). Products of ETP_F32 operands run on the
+ * float32 and rounded once when stored. The backward's dz of ETP_BF16 operands with an
+ * activation enters the products of grad_x and grad_W as two bfloat16 parts, within 2^-17
+ * of it (grad_bias sums it whole); an infinite dz gives NaN there. Products of ETP_F32 operands run on the
  * tensor cores with each operand split into three bfloat16 parts that add up to it
  * exactly; of the nine products of parts the six largest are formed (relative error
  * of a product below 2^-22). An infinite ETP_F32 operand of a linear layer therefore
