@@ -18,9 +18,14 @@
 //     bulk copies;
 //   - one warp issues the MMAs into a ring of accumulators in tensor memory;
 //   - epilogue warps add the accumulators up in registers and apply the epilogue.
-// Float32 operands are split by truncation into three bfloat16 parts x = x0 + x1 + x2
-// (8 bits each: exact), and a product is the sum of the six part products x0 w0, x0 w1,
-// x1 w0, x1 w1, x0 w2, x2 w0: what is left out is below 2^-22 of it. That is as many
+// Float32 operands are split into three bfloat16 parts x = x0 + x1 + x2 of 8 bits, and a
+// product is the sum of the six part products x0 w0, x0 w1, x1 w0, x1 w1, x0 w2, x2 w0.
+// x0 is x truncated (rounding would turn the largest floats into infinities), x1 the rest
+// rounded, x2 what is left. For x in [1, 2): x1 <= 2^-7, |x2| <= 2^-16 and a multiple of
+// 2^-23, so the three are exact, and what is left out, x1 w2 + x2 w1 + x2 w2, is below 2^-22
+// of the product and of either sign (with x1 truncated: up to 2^-21 and always towards
+// zero). Exact holds from |x| = 2^-110 up; below it x2 ends at bfloat16's smallest
+// subnormal, and the parts are within 2^-133 of x. The six are as many
 // MMAs as three TF32 products, at twice the mantissa of the smallest terms kept and in
 // three quarters of the space, and both layouts are available to 16-bit types.
 // The tensor core truncates when it adds to its accumulator; so a float32 stage starts
@@ -274,15 +279,17 @@ __device__ __forceinline__ uint32_t high_pair(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 
-// The parts of N floats, part after part, as bf16 pairs: emit(p, pairs). Three truncated
-// parts of a float32 operand, or NP rounded parts, each of what is left by those before it.
+// The parts of N floats, part after part, as bf16 pairs: emit(p, pairs). NP rounded parts,
+// each of what is left by those before it; a float32 operand's first is truncated, and its
+// last has nothing to round.
 template <typename T, int NP, int N, typename Emit>
 __device__ __forceinline__ void split_parts(float (&v)[N], Emit&& emit) {
     uint32_t w[N / 2];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
 #pragma unroll
-        for (int j = 0; j < N; j += 2) w[j / 2] = sizeof(T) == 4 ? high_pair(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
+        for (int j = 0; j < N; j += 2)
+            w[j / 2] = sizeof(T) == 4 && p != 1 ? high_pair(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
         emit(p, w);
         if (p + 1 < NP)
 #pragma unroll

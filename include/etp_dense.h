@@ -24,8 +24,9 @@
  * activation enters the products of grad_x and grad_W as two bfloat16 parts, within 2^-17
  * of it (grad_bias sums it whole); an infinite dz gives NaN there. Products of ETP_F32 operands run on the
  * tensor cores with each operand split into three bfloat16 parts that add up to it
- * exactly; of the nine products of parts the six largest are formed (relative error
- * of a product below 2^-22). An infinite ETP_F32 operand of a linear layer therefore
+ * exactly (from 2^-110 up in magnitude; below, to within 2^-133); of the nine products
+ * of parts the six largest are formed (what is left out is below 2^-22 of a product, of
+ * either sign). An infinite ETP_F32 operand of a linear layer therefore
  * gives NaN (not an infinity) in the outputs that it enters.
  *
  * Ownership and execution, errors: as in etp.h. The caller owns every buffer;

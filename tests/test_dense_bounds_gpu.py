@@ -1,6 +1,10 @@
 """Sharper bounds of the dense row operators on the GPU: single products, non-finite rows.
 
 The tolerances count:
+  - a float32 operand is split into three bfloat16 parts: truncated, rounded, and the rest. With the leading bit 1 the
+    second is at most 2^-7 and the third at most 2^-16, so what the six products leave out is below 2^-22 of a
+    product; the last of the six is added with one truncation (2^-23), those before it are 2^-6 of it and smaller.
+    The parts add up to the operand exactly from 2^-110 up; below, to within 2^-133 (bfloat16's smallest subnormal);
   - the backward's dz of bfloat16 operands is two bfloat16 parts: within 2^-16 of it;
   - storing rounds by half a step (torch.finfo(t).eps / 2).
 """
@@ -43,3 +47,54 @@ def test_bfloat16_backward_keeps_the_activations_gradient(M, K, N):
     base._close(gW, rW, (8 + M / 8) * 2.0**-23 * (xa.T @ dz) + xa.T @ off, "grad_W")
     base._close(gb, rb, (8 + M / 8) * 2.0**-23 * dz.sum(0) + 2.0**-20 * ((1 + np.abs(zn)) * np.abs(gn)).sum(0), "grad_bias")
     assert etp.device_fault() == 0
+
+
+def _dropped(x, w):
+    """What the six part products of float32 x and w leave out (float64)."""
+    def parts(v):
+        p0 = (v.contiguous().view(torch.int32) & -65536).view(torch.float32)
+        p1 = (v - p0).bfloat16().float()
+        return p0.double(), p1.double(), (v - p0 - p1).double()
+
+    a, b = parts(x), parts(w)
+    return (a[1] * b[2] + a[2] * b[1] + a[2] * b[2]).abs()
+
+
+@pytest.mark.parametrize("M,N", [(1, 1), (130, 40), (40000, 256)])
+def test_float32_single_products(M, N):
+    """One product per output (every other term zero), at mantissas whose dropped parts are largest: no more is
+    missing than the split drops, and twice a truncation of the last addition."""
+    worst = [1 + 2.0**-7 - 2.0**-23, 1 + 2.0**-7 - 2.0**-16, 1 + 2.0**-7 - 2.0**-15 + 2.0**-23, 1 + 2.0**-8 + 2.0**-16 - 2.0**-23,
+             2 - 2.0**-23, 1 + 2.0**-23, 1.0, 1 + 2.0**-7 - 2.0**-15 - 2.0**-16, -(1 + 2.0**-7 - 2.0**-17 + 2.0**-22)]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M)
+    pick = lambda *s: torch.tensor(worst, device="cuda")[torch.randint(0, len(worst), s, generator=gen, device="cuda")]
+
+    def check(got, a, b):
+        want, dropped = a.double() * b.double(), _dropped(a, b)
+        assert bool((dropped < 2.0**-22 * want.abs()).all())
+        assert bool(((got.double() - want).abs() <= dropped + (2.0**-22 + 2.0**-28) * want.abs()).all())
+
+    x, W, g = pick(M, 1), pick(1, N), pick(M, N)
+    x[0], W[0, 0], g[0, 0] = worst[0], worst[0], worst[0]
+    check(etp.linear_forward(x, W), x, W)
+    # grad_x: one column of grad_out that is not zero; grad_W: one row
+    g1 = torch.zeros_like(g)
+    g1[:, 0] = g[:, 0]
+    check(etp.linear_backward(x, W, g1, want=("x",))[0], g1[:, :1], W[:, :1])
+    g0 = torch.zeros_like(g)
+    g0[M // 2] = g[0]
+    check(etp.linear_backward(x, W, g0, want=("W",))[1], x[M // 2:M // 2 + 1], g0[M // 2:M // 2 + 1])
+
+
+def test_float32_operands_of_all_magnitudes():
+    """Subnormal and tiny operands against large ones: the operand to 2^-133, then the products' tolerance."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    exps = torch.arange(-149, 20, device="cuda", dtype=torch.float64)
+    x = (2.0**exps * (1 + torch.rand(len(exps), generator=gen, device="cuda", dtype=torch.float64))).float()[:, None]
+    x = torch.cat([x, -x, torch.tensor([[2.0**-120 * (1 + 2.0**-14)], [2.0**-126], [2.0**-149], [0.0]], device="cuda")])
+    W = torch.tensor([[2.0**100, -(2.0**99) * (1 + 2.0**-7 - 2.0**-23), 1.5 * 2.0**80]], device="cuda")
+    want = x.double() * W.double()
+    tol = (2.0**-21 + 2.0**-28) * want.abs() + 2.0**-133 * W.double().abs()
+    assert bool(((etp.linear_forward(x, W).double() - want).abs() <= tol).all())
