@@ -115,8 +115,9 @@ __global__ void __launch_bounds__(kThreads)
                         q = fmaf(v[u][i][j], v[u][i][j], q);
                     }
             const float rest = __fdiv_rn(team_sum<BLOCK>(e, team, red), (float)C);
-            const float var = fmaxf(__fdiv_rn(team_sum<BLOCK>(q, team, red), (float)C) - rest * rest, 0.f);
-            const float rs = 1.f / sqrtf(var + eps);
+            const float var = __fdiv_rn(team_sum<BLOCK>(q, team, red), (float)C) - rest * rest;
+            // (rounding may leave it below zero; a NaN stays one)
+            const float rs = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
             if (row[u] < 0) continue;
             T* os = static_cast<T*>(out.p) + out.offset(map, row[u]);
 #pragma unroll

@@ -18,6 +18,7 @@ from oracle import dense
 
 pytestmark = pytest.mark.gpu
 
+DTYPES = base.DTYPES
 _np, _rand = base._np, base._rand
 
 
@@ -98,3 +99,20 @@ def test_float32_operands_of_all_magnitudes():
     want = x.double() * W.double()
     tol = (2.0**-21 + 2.0**-28) * want.abs() + 2.0**-133 * W.double().abs()
     assert bool(((etp.linear_forward(x, W).double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("C", [1, 31, 64, 515, 1024, 2056])
+def test_layer_norm_statistics_of_non_finite_rows(C, dtype):
+    """A row with a NaN or an infinity has no statistics: mean is not finite, rstd is NaN, gradients of it are NaN."""
+    normal = _rand(C)
+    x, g = normal(40, C, dtype=dtype), normal(40, C, dtype=dtype)
+    want = etp.layer_norm_forward(x)
+    bad = x.clone()
+    bad[3, C // 2], bad[17, 0], bad[39, C - 1] = float("nan"), float("inf"), -float("inf")
+    rows, rest = [3, 17, 39], [r for r in range(40) if r not in (3, 17, 39)]
+    out, mean, rstd = etp.layer_norm_forward(bad)
+    assert bool(out[rows].isnan().all()) and not bool(mean[rows].isfinite().any()) and bool(rstd[rows].isnan().all())
+    assert all(torch.equal(a[rest], b[rest]) for a, b in zip((out, mean, rstd), want))
+    gx = etp.layer_norm_backward(bad, None, mean, rstd, g, want=("x",))[0]
+    assert bool(gx[rows].isnan().all()) and bool(gx[rest].isfinite().all())
