@@ -439,6 +439,7 @@ class _Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("group_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
 
 
+_INT_MAX = 2**31 - 1
 _DENSE_TYPES = {"torch.float32": ETP_F32, "torch.bfloat16": ETP_BF16}
 _ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "silu": ACT_SILU}
 
@@ -450,6 +451,8 @@ def _dense_lead(x, channels=None):
         raise ValueError(f"x: expected [rows, channels] or [groups, rows, channels], got {shape}")
     if channels is not None and shape[-1] != channels:
         raise ValueError(f"x: expected {channels} channels, got {shape[-1]}")
+    if max(shape) > _INT_MAX:  # the C call's sizes are ints
+        raise EtpError(ETP_ERR_TOO_LARGE, "x")
     return shape[:-1], shape[-1]
 
 
@@ -547,6 +550,8 @@ def _dense_bytes(index: int, name: str, *args) -> int:
     """Bytes that the size function `name` answers for these sizes on device `index` (they depend on nothing else)."""
     import torch
 
+    if max(args) > _INT_MAX or min(args) < -_INT_MAX:
+        raise EtpError(ETP_ERR_TOO_LARGE, name)
     b = ctypes.c_size_t()
     with torch.cuda.device(index):
         _check(getattr(_load(), name)(*args, ctypes.byref(b)), name)

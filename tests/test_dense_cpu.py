@@ -184,3 +184,19 @@ def test_blocks_of_one_feature_tensor_do_not_overlap():
     assert not etp._overlap(f[:2], f[2:]) and etp._overlap(f[:3], f[2:])
     assert not etp._overlap(f[:0], f) and not etp._overlap(f[:, 0, :4], f[:, 0, 4:])
     assert etp._overlap(f[:, 0, :5], f[:, 0, 4:])
+
+
+def test_sizes_beyond_an_int_are_refused(lib):
+    """Sizes that the C call's ints do not hold are refused, not taken modulo 2^32."""
+    W, one, many = torch.zeros(4, 8), torch.zeros(1, 4), (1 << 32) + 3
+    for call in (lambda: etp.linear_forward(one.expand(many, 4), W), lambda: etp.linear_forward(one.expand(2, many, 4), W),
+                 lambda: etp.linear_backward(one.expand(many, 4), W, torch.zeros(1, 8).expand(many, 8), want=("bias",)),
+                 lambda: etp.layer_norm_forward(one.expand(many, 4)),
+                 lambda: etp.layer_norm_forward(torch.zeros(1, 1).expand(2, many)),
+                 lambda: etp.layer_norm_backward(one.expand(many, 4), None, None, None, one.expand(many, 4)),
+                 lambda: etp.linear_workspace_size(many, 4, 8, device="cuda:0"),
+                 lambda: etp.linear_workspace_size(4, 4, many, device="cuda:0"),
+                 lambda: etp.layer_norm_workspace_size(4, many, device="cuda:0")):
+        with pytest.raises(etp.EtpError) as e:
+            call()
+        assert e.value.status == LARGE
