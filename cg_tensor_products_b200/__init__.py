@@ -613,6 +613,15 @@ def _dense_outputs(outs, ins, in_place=()):
                 raise ValueError(f"{n} must not overlap {m}")
 
 
+def _dense_want(want, *names):
+    """The gradients asked for (names, or one name), each of which must be one of `names`."""
+    want = (want,) if isinstance(want, str) else tuple(want)
+    for w in want:
+        if w not in names:
+            raise ValueError(f"want: expected some of {names}, got {w!r}")
+    return want
+
+
 def _check_linear(x, W, activation):
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation: expected 'none' or 'silu', got {activation!r}")
@@ -661,6 +670,7 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
     unwanted ones are None. z: what linear_forward kept (needed for 'silu'). The residual's gradient is grad_out."""
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
+    want = _dense_want(want, "x", "W", "bias")
     K, N = W.shape
     dtype, (lead, _) = x.dtype, _dense_lead(x, K)
     if act == ACT_NONE:
@@ -729,6 +739,7 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
     import torch
 
     code = _dense_type(x)
+    want = _dense_want(want, "x", "weight", "bias")
     dtype, (lead, C) = x.dtype, _dense_lead(x)
     xr, gr = _dense_rows(x, "x", dtype, lead, C), _dense_rows(grad_out, "grad_out", dtype, lead, C)
     wp = _dense_vector(weight, "weight", dtype, C)

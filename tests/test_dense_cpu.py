@@ -200,3 +200,16 @@ def test_sizes_beyond_an_int_are_refused(lib):
         with pytest.raises(etp.EtpError) as e:
             call()
         assert e.value.status == LARGE
+
+
+def test_unknown_gradients_are_refused(lib):
+    x, W, g, m = torch.zeros(6, 4), torch.zeros(4, 8), torch.zeros(6, 8), torch.zeros(6)
+    for want in (("x", "w"), ("weight",), "bais", ("bias", None), "xW"):
+        with pytest.raises(ValueError, match="want: expected some of"):
+            etp.linear_backward(x, W, g, want=want)
+    for want in (("x", "W"), "gamma", ("weights",)):
+        with pytest.raises(ValueError, match="want: expected some of"):
+            etp.layer_norm_backward(x, None, m, m, x, want=want)
+    for want in (("x",), "bias", ["W", "bias"], ()):  # these get as far as the device check
+        with pytest.raises(ValueError, match="no CPU path"):
+            etp.linear_backward(x, W, g, want=want)
