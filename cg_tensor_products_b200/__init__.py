@@ -577,26 +577,37 @@ def _dense_workspace(index: int, workspace, stream, name: str, *args):
         return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
 
 
-def _span(t):
-    """Elements from the first to one past the last of t."""
-    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+def _boxes_meet(d: int, dims) -> bool:
+    """Whether two boxes of elements share one. Box a starts at 0, box b at d; dims, from the outermost in: (stride,
+    a's size, b's size), the last of stride 1. A stride that does not clear what lies inside it: True (they may)."""
+    s, na, nb = dims[0]
+    if len(dims) == 1:
+        return -nb < d < na
+    inside = [1 + sum((n[i] - 1) * n[0] for n in dims[1:]) for i in (1, 2)]
+    if s < max(inside):
+        return True
+    q, r = divmod(d, s)  # b's slot of index j is a's slot q + j, shifted by r, and reaches into the next
+    return any(-nb < k < na and _boxes_meet(e, dims[1:]) for k, e in ((q, r), (q + 1, r - s)))
 
 
 def _overlap(a, b) -> bool:
-    """Whether the tensors may share memory. Two blocks of one feature tensor (equal group strides)
-    whose channel ranges are apart do not."""
+    """Whether the tensors may share memory: not where their address ranges are apart, nor two views of one feature
+    tensor that have no element in common, such as other ranks or other channels of the same nodes."""
     if a is None or b is None or not a.numel() or not b.numel():
         return False
     pa, pb, es = a.data_ptr(), b.data_ptr(), a.element_size()
-    if pa + _span(a) * es <= pb or pb + _span(b) * b.element_size() <= pa:
+    end = lambda t: t.data_ptr() + (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size()
+    if end(a) <= pb or end(b) <= pa:
         return False
-    gs = a.stride(0)
-    if a.dim() >= 2 and b.dim() >= 2 and es == b.element_size() and gs == b.stride(0) and (pb - pa) % es == 0:
-        sa, sb = (_span(t) - (t.shape[0] - 1) * gs for t in (a, b))
-        d = ((pb - pa) // es) % gs if gs else 0
-        if gs and d >= sa and d + sb <= gs:
-            return False
-    return True
+    if es != b.element_size() or (pb - pa) % es:
+        return True
+    dims = {1: [1, 1]}  # stride: a's and b's sizes along it
+    for i, t in enumerate((a, b)):
+        for s, n in zip(t.stride(), t.shape):
+            if s and n > 1:
+                dims.setdefault(s, [1, 1])[i] += n - 1
+    dims = sorted(((s, *n) for s, n in dims.items()), reverse=True)
+    return _boxes_meet((pb - pa) // es, dims)
 
 
 def _same_rows(a, b) -> bool:

@@ -116,3 +116,27 @@ def test_layer_norm_statistics_of_non_finite_rows(C, dtype):
     assert all(torch.equal(a[rest], b[rest]) for a, b in zip((out, mean, rstd), want))
     gx = etp.layer_norm_backward(bad, None, mean, rstd, g, want=("x",))[0]
     assert bool(gx[rows].isnan().all()) and bool(gx[rest].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_outputs_beside_their_inputs(dtype):
+    """Channels of one rank written from other channels of the same rows."""
+    normal = _rand(31)
+    f = normal(300, 16, 128, dtype=dtype)
+    keep, W, gamma = f.clone(), normal(64, 48, dtype=dtype), normal(64, dtype=dtype)
+    a, b, c = f[:, 4:9, :64], f[:, 4:9, 64:112], f[:, 4:9, 64:]
+    want = etp.linear_forward(a, W)
+    etp.linear_forward(a, W, out=b)
+    assert torch.equal(b, want)
+    f.copy_(keep)
+    want = etp.layer_norm_forward(a, gamma)
+    etp.layer_norm_forward(a, gamma, out=c)
+    assert torch.equal(c, want[0])
+    f.copy_(keep)
+    gx = etp.layer_norm_backward(c, gamma, *want[1:], a, want=("x",))[0]
+    etp.layer_norm_backward(c, gamma, *want[1:], f[:, 9:14, :64].copy_(a), want=("x",), grad_x=a)
+    assert torch.equal(a, gx)
+    rest = [d for d in range(16) if not 4 <= d < 14]
+    assert torch.equal(f[:, rest], keep[:, rest])
+    with pytest.raises(ValueError, match="must not overlap"):
+        etp.linear_forward(a, W, out=f[:, 4:9, 63:111])

@@ -213,3 +213,25 @@ def test_unknown_gradients_are_refused(lib):
     for want in (("x",), "bias", ["W", "bias"], ()):  # these get as far as the device check
         with pytest.raises(ValueError, match="no CPU path"):
             etp.linear_backward(x, W, g, want=want)
+
+
+def test_overlap_is_told_from_interleaving():
+    """Views of one buffer share an element exactly where the brute force finds one; other strides are only refused."""
+    f = torch.zeros(5, 16, 8)
+    assert not etp._overlap(f[:, 1:4, :4], f[:, 1:4, 4:]) and not etp._overlap(f[:, 1:4, 4:], f[:, 2:9, :4])
+    assert etp._overlap(f[:, 1:4, :5], f[:, 3:9, 4:]) and not etp._overlap(f[1:2, 1:4], f[1:2, 4:9])
+    gen = torch.Generator().manual_seed(0)
+    r = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=gen))
+    buf = torch.zeros(400)
+    for _ in range(4000):
+        rs = r(1, 9)
+        gs = rs * r(1, 6) + (r(0, 3) if r(0, 2) else 0)
+        views = [(r(0, 120), (r(1, 5), r(1, 5), r(1, 9))) for _ in range(2)]
+        a, b = (buf[o:].as_strided(n, (gs, rs, 1)) for o, n in views)
+        els = lambda o, n: {o + i * gs + j * rs + c for i in range(n[0]) for j in range(n[1]) for c in range(n[2])}
+        sets = [els(o, n) for o, n in views]
+        nested = all(n[2] <= rs and (n[1] - 1) * rs + n[2] <= gs for _, n in views)
+        flat = els(views[0][0], (views[0][1][0], 1, views[0][1][2]))
+        for got, meet in ((etp._overlap(a, b), bool(sets[0] & sets[1])), (etp._overlap(a[:, 0], b), bool(flat & sets[1])),
+                          (etp._overlap(b.transpose(0, 1), a.transpose(0, 1)), bool(sets[0] & sets[1]))):
+            assert got == meet if nested else got >= meet
