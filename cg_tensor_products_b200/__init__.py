@@ -10,6 +10,9 @@ tensors must live on a CUDA device, and a missing library raises.
     rev_ptr, rev_perm, dst = build_reverse_csr(N, row_ptr, src)
     gx, gw, gr = backward(plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, grad_out)
 
+A call given stream=s runs on s and allocates there what it creates; results may be used on s, or on the caller's
+current stream once that waits for s. Inputs have to be ready on s and alive until it has passed the call.
+
 The dense row operators (include/etp_dense.h) need no plan; they read blocks of node features in place:
 
     h, mean, rstd = layer_norm_forward(x[:, :1], weight, bias)
@@ -132,6 +135,25 @@ def _need_cuda(*ts):
         elif t.device != dev:
             raise ValueError(f"tensors on different devices ({dev}, {t.device})")
     return dev
+
+
+def _on_stream(stream, t, fn, *args):
+    """fn(*args) with `stream`, which must belong to t's device, as the current one: the tensors that it allocates are
+    that stream's. What it returns of them may be used on the caller's current stream too, so their memory is not
+    given to later work before that stream has passed the point where they are dropped."""
+    import torch
+
+    if stream.device != t.device:
+        raise ValueError(f"{fn.__name__}: stream on {stream.device}, tensors on {t.device}")
+    caller = torch.cuda.current_stream(t.device)
+    if caller == stream:
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    for r in result if isinstance(result, tuple) else (result,):
+        if r is not None and not any(r is a for a in args):
+            r.record_stream(caller)
+    return result
 
 
 def _launch(dev, where: str, fn, *args, stream=None):
@@ -526,16 +548,11 @@ def _dense_device(x, *ts):
     return index
 
 
-def _dense_call(index: int, where: str, fn, *args, stream=None):
-    """fn(*args, stream) with device `index` current, on torch's current stream of it or the caller's."""
+def _dense_call(index: int, where: str, fn, *args):
+    """fn(*args, stream) with device `index` current, on torch's current stream of it."""
     import torch
 
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        if stream.device.index != index:
-            raise ValueError(f"{where}: stream on {stream.device}, tensors on cuda:{index}")
-        raw = stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:  # switching costs more than a small launch
         status = fn(*args, raw)
     else:
@@ -558,9 +575,8 @@ def _dense_bytes(index: int, name: str, *args) -> int:
     return b.value
 
 
-def _dense_workspace(index: int, workspace, stream, name: str, *args):
-    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any. A new one
-    belongs to the call's stream: its memory is given to later work of that stream alone."""
+def _dense_workspace(index: int, workspace, name: str, *args):
+    """(workspace or None, its bytes): the caller's, checked, or a new one when the call needs any."""
     if workspace is not None:
         _expect(workspace, "workspace", "uint8", (None,))
         if not workspace.is_contiguous():
@@ -571,10 +587,7 @@ def _dense_workspace(index: int, workspace, stream, name: str, *args):
         return None, 0
     import torch
 
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
+    return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index)), n
 
 
 def _boxes_meet(d: int, dims) -> bool:
@@ -655,6 +668,8 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     for all. activation: 'none' or 'silu'. save_z=True (or z given) also keeps z = x W + bias for linear_backward:
     returns (out, z). out may be residual itself. workspace: uint8 device tensor of linear_workspace_size bytes
     (allocated when None)."""
+    if stream is not None:
+        return _on_stream(stream, x, linear_forward, x, W, bias, activation, residual, save_z, z, out, workspace)
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
     K, N = W.shape
@@ -669,9 +684,9 @@ def linear_forward(x, W, bias=None, activation="none", residual=None, save_z=Fal
     z, zr = (z, _dense_rows(z, "z", dtype, lead, N)) if z is not None or not save_z else _dense_new(x, lead, N)
     index = _dense_device(x, W, bias, residual, z, out, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
-    workspace, nbytes = _dense_workspace(index, workspace, stream, "etp_linear_workspace_size", code, groups, per, K, N, 0)
+    workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 0)
     _dense_call(index, "etp_linear_forward", _load().etp_linear_forward, code, groups, per, K, N, xr, Wp, bp, act, rr,
-                zr, orow, _ptr(workspace), nbytes, stream=stream)
+                zr, orow, _ptr(workspace), nbytes)
     return out if z is None else (out, z)
 
 
@@ -679,6 +694,9 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
                     grad_bias=None, workspace=None, stream=None):
     """(grad_x, grad_W, grad_bias) of linear_forward for the cotangent grad_out (launches etp_linear_backward);
     unwanted ones are None. z: what linear_forward kept (needed for 'silu'). The residual's gradient is grad_out."""
+    if stream is not None:
+        return _on_stream(stream, x, linear_backward, x, W, grad_out, z, activation, want, grad_x, grad_W, grad_bias,
+                          workspace)
     code = _dense_type(x)
     act = _check_linear(x, W, activation)
     want = _dense_want(want, "x", "W", "bias")
@@ -703,9 +721,9 @@ def linear_backward(x, W, grad_out, z=None, activation="none", want=("x", "W", "
     gWp, gbp = _dense_vector(grad_W, "grad_W", dtype, K, N), _dense_vector(grad_bias, "grad_bias", dtype, N)
     index = _dense_device(x, W, grad_out, z, grad_x, grad_W, grad_bias, workspace)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
-    workspace, nbytes = _dense_workspace(index, workspace, stream, "etp_linear_workspace_size", code, groups, per, K, N, 1)
+    workspace, nbytes = _dense_workspace(index, workspace, "etp_linear_workspace_size", code, groups, per, K, N, 1)
     _dense_call(index, "etp_linear_backward", _load().etp_linear_backward, code, groups, per, K, N, xr, Wp, act, zr, gr,
-                gxr, gWp, gbp, _ptr(workspace), nbytes, stream=stream)
+                gxr, gWp, gbp, _ptr(workspace), nbytes)
     return grad_x, grad_W, grad_bias
 
 
@@ -715,6 +733,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     [groups, rows]. out may be x itself."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, x, layer_norm_forward, x, weight, bias, eps, out, mean, rstd)
     code = _dense_type(x)
     dtype, (lead, C) = x.dtype, _dense_lead(x)
     xr = _dense_rows(x, "x", dtype, lead, C)
@@ -731,7 +751,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, out=None, mean=None,
     index = _dense_device(x, weight, bias, out, mean, rstd)
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
     _dense_call(index, "etp_layer_norm_forward", _load().etp_layer_norm_forward, code, groups, per, C, float(eps), xr,
-                wp, bp, orow, mp, rp, stream=stream)
+                wp, bp, orow, mp, rp)
     return out, mean, rstd
 
 
@@ -749,6 +769,9 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
     returned. grad_x may be grad_out or x itself."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, x, layer_norm_backward, x, weight, mean, rstd, grad_out, want, grad_x, grad_weight,
+                          grad_bias, workspace)
     code = _dense_type(x)
     want = _dense_want(want, "x", "weight", "bias")
     dtype, (lead, C) = x.dtype, _dense_lead(x)
@@ -771,9 +794,9 @@ def layer_norm_backward(x, weight, mean, rstd, grad_out, want=("x", "weight", "b
     groups, per = lead if len(lead) == 2 else (lead[0], 1)
     nbytes = 0
     if grad_weight is not None or grad_bias is not None:
-        workspace, nbytes = _dense_workspace(index, workspace, stream, "etp_layer_norm_workspace_size", code, groups, per, C)
+        workspace, nbytes = _dense_workspace(index, workspace, "etp_layer_norm_workspace_size", code, groups, per, C)
     _dense_call(index, "etp_layer_norm_backward", _load().etp_layer_norm_backward, code, groups, per, C, xr, wp,
-                mp, rp, gr, gxr, gwp, gbp, _ptr(workspace) if nbytes else None, nbytes, stream=stream)
+                mp, rp, gr, gxr, gwp, gbp, _ptr(workspace) if nbytes else None, nbytes)
     return grad_x, grad_weight, grad_bias
 
 

@@ -140,3 +140,58 @@ def test_outputs_beside_their_inputs(dtype):
     assert torch.equal(f[:, rest], keep[:, rest])
     with pytest.raises(ValueError, match="must not overlap"):
         etp.linear_forward(a, W, out=f[:, 4:9, 63:111])
+
+
+def _delay(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+
+
+def test_what_a_call_creates_belongs_to_its_stream():
+    """stream=s: results that are dropped at once, blocks freed on the current stream with work still queued there,
+    and results dropped while the current stream still reads them."""
+    normal = _rand(37)
+    M, K, N = 20000, 256, 192
+    x, W, g, gamma = normal(M, K), normal(K, N), normal(M, N), normal(K)
+    s, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    out, z = etp.linear_forward(x, W, None, "silu", save_z=True)
+    ln, lb = etp.layer_norm_forward(x, gamma), etp.linear_backward(x, W, g, z, "silu")
+    nb = etp.layer_norm_backward(x, gamma, *ln[1:], x)
+    torch.cuda.synchronize()
+    # all but one result dropped while s has not begun: their memory is not the current stream's to give away
+    for call, want in ((lambda: etp.layer_norm_forward(x, gamma, stream=s)[0], ln[0]),
+                       (lambda: etp.linear_backward(x, W, g, z, "silu", stream=s)[1], lb[1]),
+                       (lambda: etp.linear_forward(x, W, None, "silu", save_z=True, stream=s)[0], out),
+                       (lambda: etp.layer_norm_backward(x, gamma, *ln[1:], x, stream=s)[2], nb[2])):
+        _delay(s)
+        got = call()
+        fill = [torch.full(n, 7.0, device="cuda") for n in ((M,), (M,), (N,), (K,), (K, N), (M, N), (M, K)) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all(bool((f == 7.0).all()) for f in fill)
+        del got, fill
+    # memory freed on the current stream, whose writes to it are still queued
+    _delay(here)
+    for _ in range(3):
+        old = torch.full((M, N), 3.0, device="cuda")
+        del old
+    got = etp.linear_forward(x, W, None, "silu", stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, out)
+    # results that the current stream reads after they were dropped
+    for _ in range(2):
+        got = etp.linear_forward(x, W, None, "silu", stream=s)
+        here.wait_stream(s)
+        _delay(here)
+        later = got + 0.0
+        del got
+        other = etp.linear_forward(x, W, None, "none", stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(later, out)
+        del other, later
+    # a caller's own output, and a call that is already on its stream
+    mine = torch.empty_like(out)
+    assert etp.linear_forward(x, W, None, "silu", out=mine, stream=s) is mine
+    with torch.cuda.stream(s):
+        again = etp.linear_forward(x, W, None, "silu", stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(mine, out) and torch.equal(again, out)
