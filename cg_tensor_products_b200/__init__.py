@@ -137,6 +137,15 @@ def _need_cuda(*ts):
     return dev
 
 
+def _tensors(v):
+    """The tensors of an argument or a result: a tensor, a tuple or dict of them, a schedule."""
+    if isinstance(v, Schedule):
+        v = v.tensors()
+    elif isinstance(v, dict):
+        v = tuple(v.values())
+    return [t for t in (v if isinstance(v, tuple) else (v,)) if hasattr(t, "record_stream")]
+
+
 def _on_stream(stream, t, fn, *args):
     """fn(*args) with `stream`, which must belong to t's device, as the current one: the tensors that it allocates are
     that stream's. What it returns of them may be used on the caller's current stream too, so their memory is not
@@ -150,25 +159,19 @@ def _on_stream(stream, t, fn, *args):
         return fn(*args)
     with torch.cuda.stream(stream):
         result = fn(*args)
-    for r in result if isinstance(result, tuple) else (result,):
-        if r is not None and not any(r is a for a in args):
+    own = {id(u) for a in args for u in _tensors(a)}
+    for r in _tensors(result):
+        if id(r) not in own:
             r.record_stream(caller)
     return result
 
 
-def _launch(dev, where: str, fn, *args, stream=None):
-    """Call library function `fn(*args, stream)` with the tensors' device current.
-
-    The library launches on the current device and on the stream it is given, so
-    both must be the tensors' device: torch's current stream of `dev`, or a
-    caller's stream, which must belong to `dev`."""
+def _launch(dev, where: str, fn, *args):
+    """Call library function `fn(*args, stream)` with the tensors' device current, on torch's current stream of it."""
     import torch
 
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"{where}: stream on {s.device}, tensors on {dev}")
     with torch.cuda.device(dev):
-        _check(fn(*args, ctypes.c_void_p(s.cuda_stream)), where)
+        _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)), where)
 
 
 def _expect(t, name: str, dtype: str, shape: tuple):
@@ -244,13 +247,15 @@ def edge_frames(plan: Plan, r, frames=None, stream=None):
     """Per-edge frame records [E][FRAME_FLOATS] for r (launches etp_edge_frames)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, r, edge_frames, plan, r, frames)
     _expect(r, "r", "float32", (None, 3))
     E = r.shape[0]
     if frames is None:
         frames = torch.empty((E, FRAME_FLOATS), device=r.device, dtype=torch.float32)
     _expect(frames, "frames", "float32", (E, FRAME_FLOATS))
     dev = _need_cuda(r, frames)
-    _launch(dev, "etp_edge_frames", _load().etp_edge_frames, plan.handle, E, _ptr(r), _ptr(frames), stream=stream)
+    _launch(dev, "etp_edge_frames", _load().etp_edge_frames, plan.handle, E, _ptr(r), _ptr(frames))
     return frames
 
 
@@ -283,6 +288,8 @@ def forward(plan: Plan, row_ptr, src, r, x, w, out=None, frames=None, workspace=
     workspace: uint8 device tensor of tp_workspace_size bytes (allocated when None)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, forward, plan, row_ptr, src, r, x, w, out, frames, workspace)
     N, E = row_ptr.numel() - 1, src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(r, "r", "float32", (E, 3))
@@ -296,7 +303,7 @@ def forward(plan: Plan, row_ptr, src, r, x, w, out=None, frames=None, workspace=
     workspace = _tp_workspace(plan, N, E, False, workspace, dev)
     _need_cuda(out, workspace)
     _launch(dev, "etp_forward", _load().etp_forward, plan.handle, N, E, _ptr(row_ptr), _ptr(src), _ptr(r),
-            _ptr(frames), _ptr(x), _ptr(w), _ptr(out), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(frames), _ptr(x), _ptr(w), _ptr(out), _ptr(workspace), workspace.numel())
     return out
 
 
@@ -305,6 +312,9 @@ def backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, grad_out
     """(grad_x, grad_w, grad_r) for the cotangent grad_out (launches etp_backward); unwanted ones are None."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, backward, plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, grad_out,
+                          want, grad_x, grad_w, grad_r, frames, workspace)
     N, E = row_ptr.numel() - 1, src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(rev_ptr, "rev_ptr", "int32", (N + 1,))
@@ -330,7 +340,7 @@ def backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, grad_out
     _need_cuda(x, workspace)
     _launch(dev, "etp_backward", _load().etp_backward, plan.handle, N, E, _ptr(row_ptr), _ptr(src), _ptr(rev_ptr),
             _ptr(rev_perm), _ptr(dst), _ptr(r), _ptr(frames), _ptr(x), _ptr(w), _ptr(grad_out), _ptr(grad_x),
-            _ptr(grad_w), _ptr(grad_r), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(grad_w), _ptr(grad_r), _ptr(workspace), workspace.numel())
     return grad_x, grad_w, grad_r
 
 
@@ -338,6 +348,8 @@ def cart_forward(plan: Plan, row_ptr, src, r, x, w, out=None, workspace=None, st
     """Cartesian edge convolution (launches etp_cart_forward): x and out in independent STF components."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, cart_forward, plan, row_ptr, src, r, x, w, out, workspace)
     N, E = row_ptr.numel() - 1, src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(r, "r", "float32", (E, 3))
@@ -350,7 +362,7 @@ def cart_forward(plan: Plan, row_ptr, src, r, x, w, out=None, workspace=None, st
     workspace = _tp_workspace(plan, N, E, False, workspace, dev)
     _need_cuda(out, workspace)
     _launch(dev, "etp_cart_forward", _load().etp_cart_forward, plan.handle, N, E, _ptr(row_ptr), _ptr(src), _ptr(r),
-            _ptr(x), _ptr(w), _ptr(out), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(x), _ptr(w), _ptr(out), _ptr(workspace), workspace.numel())
     return out
 
 
@@ -361,6 +373,8 @@ def node_product(plan: Plan, x, w, K=None, cartesian=False, out=None, stream=Non
     components) couplings."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, x, node_product, plan, x, w, K, cartesian, out)
     N = x.shape[0] if x.dim() == 3 else -1
     _expect(x, "x", "float32", (N, plan.dim_in, plan.C))
     if K is None:
@@ -382,7 +396,7 @@ def node_product(plan: Plan, x, w, K=None, cartesian=False, out=None, stream=Non
             raise ValueError("out must not overlap x or w")
     dev = _need_cuda(x, out, *([w] if K > 1 else []))
     _launch(dev, "etp_node_product", _load().etp_node_product, plan.handle, N, int(K), int(bool(cartesian)),
-            _ptr(x), _ptr(w) if K > 1 else None, _ptr(out), stream=stream)
+            _ptr(x), _ptr(w) if K > 1 else None, _ptr(out))
     return out
 
 
@@ -398,6 +412,9 @@ def cart_backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, gra
     """VJP of cart_forward (launches etp_cart_backward): (grad_x, grad_w, grad_r), unwanted ones None."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, cart_backward, plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w,
+                          grad_out, want, workspace)
     N, E = row_ptr.numel() - 1, src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(rev_ptr, "rev_ptr", "int32", (N + 1,))
@@ -416,7 +433,7 @@ def cart_backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, gra
     _need_cuda(x, workspace)
     _launch(dev, "etp_cart_backward", _load().etp_cart_backward, plan.handle, N, E, _ptr(row_ptr), _ptr(src),
             _ptr(rev_ptr), _ptr(rev_perm), _ptr(dst), _ptr(r), _ptr(x), _ptr(w), _ptr(grad_out), _ptr(gx), _ptr(gw),
-            _ptr(gr), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(gr), _ptr(workspace), workspace.numel())
     return gx, gw, gr
 
 
@@ -426,6 +443,9 @@ def double_backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, g
     (the wanted ones) of <gg_x, grad_x> + <gg_w, grad_w> + <gg_r, grad_r>; None cotangents are zero."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, double_backward, plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w,
+                          grad_out, gg_x, gg_w, gg_r, want, out, workspace)
     N, E = row_ptr.numel() - 1, src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(rev_ptr, "rev_ptr", "int32", (N + 1,))
@@ -452,7 +472,7 @@ def double_backward(plan: Plan, row_ptr, src, rev_ptr, rev_perm, dst, r, x, w, g
     _launch(dev, "etp_double_backward", _load().etp_double_backward, plan.handle, N, E, _ptr(row_ptr), _ptr(src),
             _ptr(rev_ptr), _ptr(rev_perm), _ptr(dst), _ptr(r), _ptr(x), _ptr(w), _ptr(grad_out), _ptr(gg_x),
             _ptr(gg_w), _ptr(gg_r), _ptr(out.get("grad_g")), _ptr(out.get("grad_x")), _ptr(out.get("grad_w")),
-            _ptr(out.get("grad_r")), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(out.get("grad_r")), _ptr(workspace), workspace.numel())
     return out
 
 
@@ -805,6 +825,8 @@ def assemble_forces(N: int, row_ptr, rev_ptr, rev_perm, grad_r, r=None, forces=N
     The per-atom virial is computed when r is given."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, grad_r, assemble_forces, N, row_ptr, rev_ptr, rev_perm, grad_r, r, forces, virial)
     _expect(grad_r, "grad_r", "float32", (None, 3))
     E = grad_r.shape[0]
     _expect(row_ptr, "row_ptr", "int32", (N + 1,))
@@ -821,7 +843,7 @@ def assemble_forces(N: int, row_ptr, rev_ptr, rev_perm, grad_r, r=None, forces=N
         raise ValueError("virial: expected float32 with N*9 elements")
     dev = _need_cuda(row_ptr, rev_ptr, rev_perm, grad_r, r, forces, virial)
     _launch(dev, "etp_assemble_forces", _load().etp_assemble_forces, int(N), int(E), _ptr(row_ptr), _ptr(rev_ptr),
-            _ptr(rev_perm), _ptr(r), _ptr(grad_r), _ptr(forces), _ptr(virial), stream=stream)
+            _ptr(rev_perm), _ptr(r), _ptr(grad_r), _ptr(forces), _ptr(virial))
     return forces, virial
 
 
@@ -846,6 +868,8 @@ def radial_forward(plan: Plan, r, W1, W2, r_cut: float, w=None, workspace=None, 
     """w [E, P, C] = SiLU(bessel(|r|) W1) W2 (etp_radial_forward)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, r, radial_forward, plan, r, W1, W2, r_cut, w, workspace)
     _expect(r, "r", "float32", (None, 3))
     E = r.shape[0]
     _expect(W1, "W1", "float32", (None, None))
@@ -856,7 +880,7 @@ def radial_forward(plan: Plan, r, W1, W2, r_cut: float, w=None, workspace=None, 
     workspace = _radial_ws(plan, E, W1, workspace)
     dev = _need_cuda(r, W1, W2, w, workspace)
     _launch(dev, "etp_radial_forward", _load().etp_radial_forward, plan.handle, E, W1.shape[0], W1.shape[1],
-            float(r_cut), _ptr(r), _ptr(W1), _ptr(W2), _ptr(w), _ptr(workspace), workspace.numel(), stream=stream)
+            float(r_cut), _ptr(r), _ptr(W1), _ptr(W2), _ptr(w), _ptr(workspace), workspace.numel())
     return w
 
 
@@ -865,6 +889,9 @@ def radial_backward(plan: Plan, r, W1, W2, r_cut: float, grad_w, grad_r, grad_W1
     """(grad_W1, grad_W2); adds the derivative through |r| to grad_r in place (etp_radial_backward)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, r, radial_backward, plan, r, W1, W2, r_cut, grad_w, grad_r, grad_W1, grad_W2,
+                          workspace)
     _expect(r, "r", "float32", (None, 3))
     E = r.shape[0]
     _expect(W1, "W1", "float32", (None, None))
@@ -881,7 +908,7 @@ def radial_backward(plan: Plan, r, W1, W2, r_cut: float, grad_w, grad_r, grad_W1
     dev = _need_cuda(r, W1, W2, grad_w, grad_r, grad_W1, grad_W2, workspace)
     _launch(dev, "etp_radial_backward", _load().etp_radial_backward, plan.handle, E, W1.shape[0], W1.shape[1],
             float(r_cut), _ptr(r), _ptr(W1), _ptr(W2), _ptr(grad_w), _ptr(grad_W1), _ptr(grad_W2), _ptr(grad_r),
-            _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(workspace), workspace.numel())
     return grad_W1, grad_W2
 
 
@@ -897,6 +924,8 @@ def fused_forward(plan: Plan, row_ptr, src, r, x, W1, W2, r_cut: float, out=None
     (launches etp_fused_forward)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, fused_forward, plan, row_ptr, src, r, x, W1, W2, r_cut, out, workspace)
     N, E = row_ptr.numel() - 1, src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(r, "r", "float32", (E, 3))
@@ -913,7 +942,7 @@ def fused_forward(plan: Plan, row_ptr, src, r, x, W1, W2, r_cut: float, out=None
     dev = _need_cuda(row_ptr, src, r, x, W1, W2, out, workspace)
     _launch(dev, "etp_fused_forward", _load().etp_fused_forward, plan.handle, N, E, _ptr(row_ptr), _ptr(src),
             _ptr(r), _ptr(x), W1.shape[0], W1.shape[1], float(r_cut), _ptr(W1), _ptr(W2), _ptr(out),
-            _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(workspace), workspace.numel())
     return out
 
 
@@ -927,6 +956,8 @@ def build_reverse_csr(N: int, row_ptr, src, with_dst=True, workspace=None, strea
     """(rev_ptr [N+1], rev_perm [E], dst [E] or None), all int32 on the device (etp_build_reverse_csr)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, build_reverse_csr, N, row_ptr, src, with_dst, workspace)
     E = src.numel()
     _check_graph(row_ptr, src, N, E)
     dev = row_ptr.device
@@ -939,7 +970,7 @@ def build_reverse_csr(N: int, row_ptr, src, with_dst=True, workspace=None, strea
     _expect(workspace, "workspace", "uint8", (None,))
     dev = _need_cuda(row_ptr, src, rev_ptr, rev_perm, dst, workspace)
     _launch(dev, "etp_build_reverse_csr", _load().etp_build_reverse_csr, N, E, _ptr(row_ptr), _ptr(src),
-            _ptr(rev_ptr), _ptr(rev_perm), _ptr(dst), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(rev_ptr), _ptr(rev_perm), _ptr(dst), _ptr(workspace), workspace.numel())
     return rev_ptr, rev_perm, dst
 
 
@@ -948,6 +979,8 @@ def build_reverse_csr_static(N: int, row_ptr, src, with_dst=True, stream=None):
     (etp_build_reverse_csr_static; N, E <= 2^18; calls that overlap on the GPU race)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, build_reverse_csr_static, N, row_ptr, src, with_dst)
     E = src.numel()
     _check_graph(row_ptr, src, N, E)
     dev = row_ptr.device
@@ -956,7 +989,7 @@ def build_reverse_csr_static(N: int, row_ptr, src, with_dst=True, stream=None):
     dst = torch.empty(E, dtype=torch.int32, device=dev) if with_dst else None
     dev = _need_cuda(row_ptr, src, rev_ptr, rev_perm, dst)
     _launch(dev, "etp_build_reverse_csr_static", _load().etp_build_reverse_csr_static, N, E, _ptr(row_ptr),
-            _ptr(src), _ptr(rev_ptr), _ptr(rev_perm), _ptr(dst), stream=stream)
+            _ptr(src), _ptr(rev_ptr), _ptr(rev_perm), _ptr(dst))
     return rev_ptr, rev_perm, dst
 
 
@@ -985,6 +1018,8 @@ def locality_schedule(N: int, row_ptr, src, pos, cell: float, out: Schedule = No
     (etp_build_locality_schedule). out: a Schedule of the same sizes to overwrite."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, locality_schedule, N, row_ptr, src, pos, cell, out, workspace)
     E = src.numel()
     _check_graph(row_ptr, src, N, E)
     _expect(pos, "pos", "float32", (N, 3))
@@ -1001,8 +1036,7 @@ def locality_schedule(N: int, row_ptr, src, pos, cell: float, out: Schedule = No
     _expect(workspace, "workspace", "uint8", (None,))
     dev = _need_cuda(row_ptr, src, pos, workspace, *out.tensors())
     _launch(dev, "etp_build_locality_schedule", _load().etp_build_locality_schedule, N, E, _ptr(row_ptr), _ptr(src),
-            _ptr(pos), float(cell), *[_ptr(t) for t in out.tensors()], _ptr(workspace), workspace.numel(),
-            stream=stream)
+            _ptr(pos), float(cell), *[_ptr(t) for t in out.tensors()], _ptr(workspace), workspace.numel())
     return out
 
 
@@ -1010,6 +1044,8 @@ def forward_ordered(plan: Plan, sched: Schedule, src, r, x, w, out=None, frames=
     """forward() on a locality schedule (etp_forward_ordered): the same out, rows visited in schedule order."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, x, forward_ordered, plan, sched, src, r, x, w, out, frames, workspace)
     N, E = sched.N, sched.E
     _expect(src, "src", "int32", (E,))
     _expect(r, "r", "float32", (E, 3))
@@ -1024,7 +1060,7 @@ def forward_ordered(plan: Plan, sched: Schedule, src, r, x, w, out=None, frames=
     _need_cuda(out, workspace)
     _launch(dev, "etp_forward_ordered", _load().etp_forward_ordered, plan.handle, N, E, _ptr(sched.order),
             _ptr(sched.ord_ptr), _ptr(sched.ord_edge), _ptr(src), _ptr(r), _ptr(frames), _ptr(x), _ptr(w),
-            _ptr(out), _ptr(workspace), workspace.numel(), stream=stream)
+            _ptr(out), _ptr(workspace), workspace.numel())
     return out
 
 
@@ -1033,6 +1069,9 @@ def backward_ordered(plan: Plan, sched: Schedule, r, x, w, grad_out, want=("x", 
     """backward() on a locality schedule (etp_backward_ordered): the same (grad_x, grad_w, grad_r)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, x, backward_ordered, plan, sched, r, x, w, grad_out, want, grad_x, grad_w, grad_r,
+                          frames, workspace)
     N, E = sched.N, sched.E
     _expect(r, "r", "float32", (E, 3))
     _expect(frames, "frames", "float32", (E, FRAME_FLOATS))
@@ -1055,8 +1094,7 @@ def backward_ordered(plan: Plan, sched: Schedule, r, x, w, grad_out, want=("x", 
     _need_cuda(x, workspace)
     _launch(dev, "etp_backward_ordered", _load().etp_backward_ordered, plan.handle, N, E, _ptr(sched.order),
             _ptr(sched.rev_ptr), _ptr(sched.rev_perm), _ptr(sched.dst), _ptr(r), _ptr(frames), _ptr(x), _ptr(w),
-            _ptr(grad_out), _ptr(grad_x), _ptr(grad_w), _ptr(grad_r), _ptr(workspace), workspace.numel(),
-            stream=stream)
+            _ptr(grad_out), _ptr(grad_x), _ptr(grad_w), _ptr(grad_r), _ptr(workspace), workspace.numel())
     return grad_x, grad_w, grad_r
 
 
@@ -1071,9 +1109,11 @@ def validate_csr(N: int, row_ptr, src, stream=None) -> int:
     """The ETP_CSR_* bits of every problem found in the CSR (0 = valid). Synchronises the stream."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, row_ptr, validate_csr, N, row_ptr, src)
     _check_graph(row_ptr, src, N, src.numel())
     flag = torch.empty(1, dtype=torch.int32, device=row_ptr.device)
     dev = _need_cuda(row_ptr, src, flag)
     _launch(dev, "etp_validate_csr", _load().etp_validate_csr, N, src.numel(), _ptr(row_ptr), _ptr(src),
-            _ptr(flag), stream=stream)
+            _ptr(flag))
     return int(flag.item())
