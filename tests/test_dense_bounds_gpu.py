@@ -1,6 +1,6 @@
-"""Sharper bounds of the dense row operators on the GPU: single products, non-finite rows.
+"""Sharper bounds of the dense row operators on the GPU: exact row sums, single products, non-finite rows.
 
-The tolerances count:
+Where an answer is exact in every order of summation it is compared bit for bit. Elsewhere the tolerances count:
   - a float32 operand is split into three bfloat16 parts: truncated, rounded, and the rest. With the leading bit 1 the
     second is at most 2^-7 and the third at most 2^-16, so what the six products leave out is below 2^-22 of a
     product; the last of the six is added with one truncation (2^-23), those before it are 2^-6 of it and smaller.
@@ -26,6 +26,56 @@ _np, _rand = base._np, base._rand
 def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
+
+
+def _ints(gen, dtype, *shape):
+    return torch.randint(-2, 3, shape, generator=gen, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 5, 3), (515, 24, 300), (1000, 99, 37), (70001, 64, 96), (38017, 131, 257),
+                                   (40000, 256, 256), (131149, 200, 128), (65537, 40, 20)])
+def test_sums_over_rows_are_exact_on_small_integers(M, K, N, dtype):
+    """Every row counts once: sums of small integers stay exact in float32 in any order, so grad_W and grad_bias are
+    the true sums rounded once. grad_bias alone is the same."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M + K + N)
+    x, g = _ints(gen, dtype, M, K), _ints(gen, dtype, M, N)
+    W = _ints(gen, dtype, K, N)
+    gx, gW, gb = etp.linear_backward(x, W, g)
+    assert torch.equal(gx, (g.double() @ W.double().T).to(dtype))
+    assert torch.equal(gW, (x.double().T @ g.double()).to(dtype))
+    assert torch.equal(gb, g.double().sum(0).to(dtype))
+    assert torch.equal(etp.linear_backward(x, W, g, want=("bias",))[2], gb)
+    out = etp.linear_forward(x, W)
+    assert torch.equal(out, (x.double() @ W.double()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", [(70001, 4352), (131149, 33), (300000, 1)])
+def test_bias_gradient_alone(M, N, dtype):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M)
+    g = _ints(gen, dtype, M, N)
+    x, W = torch.zeros(M, 1, device="cuda", dtype=dtype), torch.zeros(1, N, device="cuda", dtype=dtype)
+    only = etp.linear_backward(x, W, g, want=("bias",))
+    assert only[0] is None and only[1] is None and torch.equal(only[2], g.sum(0, dtype=torch.float64).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(70001, 64, 96), (40000, 256, 256), (38017, 131, 257)])
+def test_sums_over_rows_through_the_activation(M, K, N, dtype):
+    """The same with dz = g silu'(0) = g / 2 (silu'(0) within 8 roundings of 1/2): one lost row moves an element by
+    1/2 or more, far above the tolerance in float32; in bfloat16 also the 2-norm of the rounded sums."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M)
+    x, g = _ints(gen, dtype, M, K), _ints(gen, dtype, M, N)
+    _, gW, gb = etp.linear_backward(x, _ints(gen, dtype, K, N), g, torch.zeros_like(g), "silu", want=("W", "bias"))
+    half = torch.finfo(dtype).eps / 2
+    for got, a, b in ((gW, x, g), (gb[None], torch.ones_like(x[:, :1]), g)):
+        want, size = a.double().T @ b.double() / 2, a.double().abs().T @ b.double().abs() / 2
+        assert bool(((got.double() - want).abs() <= half * want.abs() + 2.0**-21 * size).all())
+        assert float((got.double() - want).norm()) <= (half + 2.0**-20) * float(want.norm()) + 2.0**-21 * float(size.norm())
 
 
 @pytest.mark.parametrize("M,K,N", [(300, 99, 37), (4096, 256, 256), (5000, 64, 96), (1000, 131, 515), (2, 64, 4352),
@@ -99,6 +149,15 @@ def test_float32_operands_of_all_magnitudes():
     want = x.double() * W.double()
     tol = (2.0**-21 + 2.0**-28) * want.abs() + 2.0**-133 * W.double().abs()
     assert bool(((etp.linear_forward(x, W).double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,C", [(5000, 515), (5000, 1032), (2500, 1025), (2500, 2056), (1500, 5001), (1500, 8192), (3000, 257)])
+def test_layer_norm_several_rows_a_block(M, C, dtype):
+    """Wide rows that a whole block takes, more of them than blocks: a block's second and later rows."""
+    normal = _rand(M + C)
+    x = normal(M, C, dtype=dtype, scale=2.0, shift=0.7)
+    base._check_norm(x, normal(C, dtype=dtype, scale=0.2, shift=1.0), normal(C, dtype=dtype), normal(M, C, dtype=dtype))
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
