@@ -94,8 +94,13 @@ struct Pack<__nv_bfloat16, 8> {
 };
 
 // SiLU and its derivative in float32: s = 1 / (1 + exp(-z)), silu = z s,
-// silu' = s (1 + z (1 - s)), with the approximate 2^x and 1/x of the special function
-// unit (2 ulp and 1 ulp of their own results). Subnormal intermediates go to zero, which
+// silu' = s (1 + z (1 - s)), with exp(-z) = 2^(-z log2(e)) and the approximate 2^x and 1/x of
+// the special function unit (2 ulp and 1 ulp of their own results). The product z log2(e) is
+// rounded before 2^x, so exp is off by up to 1.25 |z| 2^-24 of itself more (the rounding, and
+// that of log2(e)): s keeps (1.25 |z| + 8) 2^-24 of its own size, which for z > 0 is mostly the
+// 1 beside exp, and for z = -20, where silu is -4e-8, 33 units of 2^-24. Carrying the low part
+// of the product along would cost four more instructions an element, for an absolute error
+// that stays below 2^-24 (1 + |z|). Subnormal intermediates go to zero, which
 // only exp(-z) for z > 87 and 1/x for z < -87 reach: s is then 1 or 0 within 2^-126.
 __device__ __forceinline__ float sigmoid(float z) {
     float e, s;

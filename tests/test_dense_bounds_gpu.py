@@ -6,6 +6,8 @@ Where an answer is exact in every order of summation it is compared bit for bit.
     product; the last of the six is added with one truncation (2^-23), those before it are 2^-6 of it and smaller.
     The parts add up to the operand exactly from 2^-110 up; below, to within 2^-133 (bfloat16's smallest subnormal);
   - the backward's dz of bfloat16 operands is two bfloat16 parts: within 2^-16 of it;
+  - exp(-z): the argument z log2(e) is rounded (2^-24 of it) and log2(e) is off by 2^-26 of itself, so exp is off by
+    1.25 |z| 2^-24 of its own size, and by 2^-22 for the approximate 2^x;
   - storing rounds by half a step (torch.finfo(t).eps / 2).
 """
 import numpy as np
@@ -149,6 +151,24 @@ def test_float32_operands_of_all_magnitudes():
     want = x.double() * W.double()
     tol = (2.0**-21 + 2.0**-28) * want.abs() + 2.0**-133 * W.double().abs()
     assert bool(((etp.linear_forward(x, W).double() - want).abs() <= tol).all())
+
+
+def test_silu_of_large_pre_activations():
+    """Relative to its own size: s = 1 / (1 + exp(-z)) within e = (1.25 |z| + 8) 2^-24 (argument, 2^x: 4, sum 1, 1/x:
+    2), silu with one rounding more; silu' = s (1 + z (1 - s)) by the same count, and as an operand of grad_x's product
+    it is split: to within 2^-133 (it falls to 2^-118 here)."""
+    z = torch.cat([torch.linspace(-86, 86, 20001, device="cuda"), -torch.logspace(-6, 1.9, 5000, device="cuda")])[:, None]
+    one = torch.ones(1, 1, device="cuda")
+    out, zz = etp.linear_forward(z, one, None, "silu", save_z=True)
+    assert torch.equal(zz, z)
+    zn = _np(z)
+    s, e = dense.sigmoid(zn), (1.25 * np.abs(zn) + 8) * 2.0**-24
+    ref = dense.act(zn, "silu")
+    assert (np.abs(_np(out) - ref) <= (e + 2.0**-24) * np.abs(ref)).all()
+    gx = etp.linear_backward(z, one, torch.ones_like(z), zz, "silu", want=("x",))[0]
+    q = 1 + zn * (1 - s)
+    slack = s * (np.abs(zn) * (s * e + 2.0**-24 * (1 - s)) + 2.0**-23 * np.abs(q) + np.abs(q) * (e + 2.0**-22))
+    assert (np.abs(_np(gx) - s * q) <= slack + 2.0**-133).all()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
