@@ -9,7 +9,9 @@
 // groups, then a warp with several groups per lane, a whole block for wide rows), so the second pass over it costs no further read. That pass takes the
 // deviations d from the rounded mean and both sum(d) and sum(d^2): the first corrects
 // the mean for its own rounding, the variance is sum(d^2) / C minus that correction
-// squared, so a large common offset of a row costs no accuracy. Channel c always belongs to the
+// squared, so a large common offset of a row costs the forward no accuracy. The backward is
+// the formula at the mean that it is given, which float32 has rounded: xh is off by up to
+// 2^-24 |mean| rstd. Channel c always belongs to the
 // same lane, so the weight gradients are summed in registers over all rows a block
 // visits; each block leaves one partial row in the workspace, and a second launch
 // adds the partial rows in block order.

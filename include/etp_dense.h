@@ -113,6 +113,9 @@ ETP_API etp_status etp_layer_norm_workspace_size(etp_dtype dtype, int groups, in
  *   xh = (x - mean) rstd;  gw = grad_out weight
  *   grad_x = rstd (gw - sum(gw) / C - xh sum(gw xh) / C)
  *   grad_weight = sum over the rows of grad_out xh;  grad_bias = sum over the rows of grad_out
+ * xh is formed from the mean as it is given, in float32: in a row whose offset is large beside
+ * its spread it is off by half a step of the mean, 2^-24 |mean| rstd, and the gradients with
+ * it (offset 1e4, spread 1: 3e-4 of grad_weight). The forward has no such error.
  * weight NULL: ones. Each gradient may be NULL (skipped). grad_x may be grad_out or x
  * itself (same data and strides). workspace: etp_layer_norm_workspace_size bytes,
  * 16-byte aligned (may be NULL when neither grad_weight nor grad_bias is wanted). */

@@ -197,6 +197,27 @@ def test_layer_norm_statistics_of_non_finite_rows(C, dtype):
     assert bool(gx[rows].isnan().all()) and bool(gx[rest].isfinite().all())
 
 
+def test_layer_norm_gradients_of_rows_with_a_large_offset():
+    """The backward takes the mean as it is stored, in float32: xh is off by half a step of it, 2^-24 |mean| rstd.
+    Against gradients from the unrounded mean."""
+    normal = _rand(2)
+    C = 200
+    x, g = normal(64, C, shift=1e4), normal(64, C)
+    _, mean, rstd = etp.layer_norm_forward(x)
+    xn, gn = _np(x), _np(g)
+    _, m64, r64 = dense.layer_norm_forward(xn)
+    gx, gw, gb = etp.layer_norm_backward(x, None, mean, rstd, g)
+    rx, rw, rb = dense.layer_norm_backward(xn, None, m64, r64, gn)
+    d = (2.0**-23 * np.abs(m64) * r64)[:, None]  # half a step of the mean, and as much for its own sum
+    ga, xh = np.abs(gn), np.abs((xn - m64[:, None]) * r64[:, None])
+    assert (np.abs(_np(gw) - rw) <= ((d + 2.0**-18 * xh) * ga).sum(0)).all()
+    assert (np.abs(_np(gb) - rb) <= 2.0**-20 * ga.sum(0)).all()
+    # r (gw - mean(gw) - xh mean(gw xh)), rstd itself within 2^-18
+    gxh = (ga * xh).mean(1, keepdims=True)
+    slack = r64[:, None] * (2.0**-18 * (ga + ga.mean(1, keepdims=True) + xh * gxh) + d * gxh + (xh + d) * d * ga.mean(1, keepdims=True))
+    assert (np.abs(_np(gx) - rx) <= slack).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_outputs_beside_their_inputs(dtype):
     """Channels of one rank written from other channels of the same rows."""
