@@ -1101,8 +1101,13 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
 // with bfloat16 alone: A is then read, and dz formed, half as often; 131072 x 256 -> 256
 // grad_x 102 us with 128, 61 us with 256; float32 parts leave no tensor memory for it).
 // float32 takes 128 columns once every SM gets two such tiles: below that its one or two
-// rounds wait for whole conversions (20480 x 128 -> 128 22.6 us with 128, 17.7 us with 64,
-// 37000 rows 24.6 / 21.5, 40000 rows 21.5 / 23.5; bfloat16 12.3 / 13.3 at 20480). And whether W
+// rounds wait for whole conversions (forward with 128 / 64 columns, on the device alone:
+// 20480 x 128 -> 128 18.8 / 13.0 us, 37000 rows 19.8 / 15.8, 40000 rows 15.0 / 18.5; bfloat16
+// 12.3 / 13.3 at 20480). The rule counts SMs without a tile, not rounds, and loses where a
+// wider tile would take fewer of them, float32 forward: 8192 x 128 -> 128 10.6 us with the 32
+// columns that it takes (64: 8.3), 2048 x 128 -> 512 10.6 (64: 8.3), 4096 x 256 -> 256 15.9 (64:
+// 12.1), 12288 x 128 -> 128 12.3 with 64 (128: 11.4), 2048 x 256 -> 1024 18.6 with 64 (128:
+// 16.6); it gains at 1024 x 128 -> 512 6.8 with 32 (64: 8.0) and 4096 x 128 -> 128 7.0 (8.2). And whether W
 // is converted ahead (an image), which pays once a CTA would convert it more than once and
 // enough row tiles share it. float32, with the image / without: 64 x 256 -> 65536 64 / 51 us,
 // 256 x 1024 -> 32768 155 / 170, 4096 x 512 -> 4096 90 / 156. bfloat16, whose image is only a
