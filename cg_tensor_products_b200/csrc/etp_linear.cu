@@ -425,7 +425,7 @@ __device__ __forceinline__ unsigned long long row_offset(const Job& job, const R
 }
 // bfloat16 pairs of a row's groups c, c + 1 (16 columns, one sector): traded between the
 // row's 4 lanes so that each stores 4 neighbouring columns and the sector is written whole
-// (grad_x: 131072 x 256 bf16 67 -> 61 us; the forward's longer epilogue loses by it, 112 -> 171 us
+// (grad_x: 131072 x 256 bf16 66 -> 58 us; the forward's longer epilogue loses by it, 112 -> 171 us
 // at 166517 x 512).
 template <int G>
 __device__ __forceinline__ void store_quads(__nv_bfloat16* row, const float2 (&v)[G], int lane) {
@@ -1099,7 +1099,7 @@ cudaError_t launch_bn(Job& j, unsigned char* image, cudaStream_t s) {
 // How the forward and grad_x products of M rows, k contracted and n output columns are
 // tiled: the widest tile that still gives every SM one, or the narrowest (256 columns
 // with bfloat16 alone: A is then read, and dz formed, half as often; 131072 x 256 -> 256
-// grad_x 102 us with 128, 61 us with 256; float32 parts leave no tensor memory for it).
+// grad_x 89 us with 128, 58 us with 256; float32 parts leave no tensor memory for it).
 // float32 takes 128 columns once every SM gets two such tiles: below that its one or two
 // rounds wait for whole conversions (forward with 128 / 64 columns, on the device alone:
 // 20480 x 128 -> 128 18.8 / 13.0 us, 37000 rows 19.8 / 15.8, 40000 rows 15.0 / 18.5; bfloat16
@@ -1163,7 +1163,7 @@ struct Ranges {
 Ranges ranges(bool bf16, int M, int K, int N) {
     Ranges r;
     r.bn = N > 64 ? 128 : N > 32 ? 64 : 32;
-    r.tall = bf16 && K > 128 && r.bn == 128 ? 2 : 1;  // (131072 x 256 -> 256: 98 us with 1, 74 us with 2)
+    r.tall = bf16 && K > 128 && r.bn == 128 ? 2 : 1;  // (131072 x 256 -> 256: 90 us with 1, 66 us with 2)
     r.tiles = ((K + r.tall * kRowsTile - 1) / (r.tall * kRowsTile)) * ((N + r.bn - 1) / r.bn);
     const int sms = sm_count();
     const int stages = (M + kRangeK - 1) / kRangeK;
