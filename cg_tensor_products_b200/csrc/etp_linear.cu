@@ -675,7 +675,8 @@ __global__ void __launch_bounds__(Warps<T, P>::kThreads, 1) etp_linear_kernel(co
 #pragma unroll
                     for (int j = 0; j < 8; ++j) bsum[j] += v[j];
                 }
-                if (ShareB::has(lt, i)) store_parts<T, Lay::kPB>(sb + ShareB::offset(lt, i), Lay::kBPart, v, sizeof(T) == 4 || job.silu);
+                if (ShareB::has(lt, i))  // (a bfloat16 cotangent without an activation has no low part)
+                    store_parts<T, Lay::kPB>(sb + ShareB::offset(lt, i), Lay::kBPart, v, sizeof(T) == 4 || job.silu);
             }
         };
         // -- operands used as they are, straight into the slot
